@@ -14,6 +14,13 @@ Functions mirror the C entry points:
     mf_set_wait_limit(...)  bounded-wait limit (and a test stall) of the tensor-core kernels
     mf_compress_workspace_size(...), mf_retrieve_path(...), mf_version()
     mf_calib_gram(...), mf_calib_solve(...), mf_calib_path(...)   (head-map calibration)
+The receiver's paged key-value cache (PagedKV):
+    mf_kv_append(...)       new tokens' keys and values into the pages
+    mf_map_key_scores(...)  -> scores every key gathered in a prefill that reused maps
+    mf_paged_decode(...)    -> O of one new token per sequence
+    mf_kv_evict(...)        -> lengths of the cache cut back by gathered weight
+    mf_paged_decode_workspace_size(...), mf_kv_evict_workspace_size(...),
+    mf_map_key_scores_workspace_size(...)
 """
 import ctypes
 import os
@@ -38,6 +45,7 @@ MF_F32, MF_BF16 = 0, 1
 MF_RETRIEVE_FORCE_SIMT = 1
 MF_RETRIEVE_O_F32 = 2
 MF_RETRIEVE_P_SPLIT = 4
+MF_DECODE_O_F32 = 1
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -84,6 +92,38 @@ class CalibDesc(ctypes.Structure):
     _fields_ = [("sender_maps", _P), ("receiver_maps", _P), ("dtype", ctypes.c_int),
                 ("sender_seq_offset", _P), ("receiver_seq_offset", _P), ("seqlens", _P),
                 ("nseq", _I32), ("h_s", _I32), ("h_r", _I32), ("B", _I32), ("gram", _P)]
+
+
+class PagedKVDesc(ctypes.Structure):
+    _fields_ = [("K", _P), ("V", _P), ("dtype", ctypes.c_int), ("page_stride", _I64),
+                ("n_pages", _I32), ("page_size", _I32), ("max_pages", _I32), ("h_kv", _I32),
+                ("d", _I32), ("block_table", _P), ("seq_lens", _P), ("nseq", _I32),
+                ("max_len", _I32)]
+
+
+class PagedDecodeDesc(ctypes.Structure):
+    _fields_ = [("kv", PagedKVDesc), ("Q", _P), ("q_stride", _I64), ("h_r", _I32),
+                ("scale", ctypes.c_float), ("O", _P), ("lse", _P), ("score_in", _P),
+                ("score_out", _P), ("score_stride", _I64), ("flags", _I32)]
+
+
+class KvAppendDesc(ctypes.Structure):
+    _fields_ = [("kv", PagedKVDesc), ("K_new", _P), ("V_new", _P), ("new_stride", _I64),
+                ("total_new", _I64), ("cu_seqlens_new", _P), ("max_new", _I32), ("n_seen", _P),
+                ("score", _P), ("pos", _P), ("score_stride", _I64)]
+
+
+class KvEvictDesc(ctypes.Structure):
+    _fields_ = [("kv", PagedKVDesc), ("score_in", _P), ("pos_in", _P), ("score_out", _P),
+                ("pos_out", _P), ("score_stride", _I64), ("n_seen", _P), ("budget", _I32),
+                ("sink", _I32), ("window", _I32), ("seq_lens_out", _P)]
+
+
+class KeyScoresDesc(ctypes.Structure):
+    _fields_ = [("bsr", BsrDesc), ("n_rows", _I64), ("map_dtype", ctypes.c_int), ("h_s", _I32),
+                ("B", _I32), ("W", _P), ("h_r", _I32), ("h_kv", _I32), ("cu_seqlens", _P),
+                ("qblock_base", _P), ("nseq", _I32), ("max_seqlen", _I32), ("score", _P),
+                ("score_stride", _I64)]
 
 
 _lib.mf_compress_workspace_size.argtypes = [ctypes.POINTER(CompressDesc), ctypes.POINTER(ctypes.c_size_t)]
@@ -135,8 +175,19 @@ _lib.mf_calib_solve.argtypes = [_P, _I32, _I32, ctypes.c_double, _P, _P, _P]
 _lib.mf_calib_solve.restype = ctypes.c_int
 _lib.mf_calib_path.argtypes = [ctypes.POINTER(CalibDesc)]
 _lib.mf_calib_path.restype = ctypes.c_int
+for _n, _s in (("mf_paged_decode", PagedDecodeDesc), ("mf_kv_evict", KvEvictDesc),
+               ("mf_map_key_scores", KeyScoresDesc)):
+    _f = getattr(_lib, _n + "_workspace_size")
+    _f.argtypes = [ctypes.POINTER(_s), ctypes.POINTER(ctypes.c_size_t)]
+    _f.restype = ctypes.c_int
+    _f = getattr(_lib, _n)
+    _f.argtypes = [ctypes.POINTER(_s), _P, ctypes.c_size_t, _P]
+    _f.restype = ctypes.c_int
+_lib.mf_kv_append.argtypes = [ctypes.POINTER(KvAppendDesc), _P]
+_lib.mf_kv_append.restype = ctypes.c_int
 
-for _k, _s in ((0, CompressDesc), (1, BsrDesc), (2, RetrieveDesc), (3, CalibDesc)):
+for _k, _s in ((0, CompressDesc), (1, BsrDesc), (2, RetrieveDesc), (3, CalibDesc),
+               (5, PagedDecodeDesc), (6, KvAppendDesc), (8, KvEvictDesc), (9, KeyScoresDesc)):
     if _lib.mf_abi_struct_size(_k) != ctypes.sizeof(_s):
         raise ImportError(f"libmf.so struct {_s.__name__} size mismatch: rebuild the library")
 
@@ -546,3 +597,242 @@ def choose_sender_layer(residuals_per_candidate: Sequence[torch.Tensor]) -> int:
     the smallest total residual (one residual vector per candidate, from mf_calib_solve)."""
     totals = [float(r.double().sum()) for r in residuals_per_candidate]
     return min(range(len(totals)), key=lambda k: (totals[k], k))
+
+
+# ----------------------------------------------------------------------------- paged cache
+
+def _need(t, what, dtype, shape=None, device=None, contiguous=True):
+    """Refuse a tensor the kernels could not read as described."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the call's other tensors on {device}")
+    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple('*' if n is None else n for n in shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _row_stride(t, what):
+    """Elements between the rows (dim 0) of t, whose other dims must be dense; 0 for one row."""
+    step = 1
+    for k in range(t.dim() - 1, 0, -1):
+        if t.shape[k] != 1 and t.stride(k) != step:
+            raise ValueError(f"{what}: the dims after the first must be dense")
+        step *= t.shape[k]
+    return t.stride(0) if t.shape[0] > 1 and t.numel() else 0
+
+
+def _scratch(need, workspace, device, stream):
+    """The caller's workspace, or one allocated here and kept from reuse until `stream` is done."""
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        return workspace
+    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None:
+        workspace.record_stream(stream)
+    return workspace
+
+
+def _enqueue(name, d, workspace, device, stream):
+    """Workspace and launch of one call on its tensors' device, on `stream` or the current one."""
+    fn = getattr(_lib, name)
+    with torch.cuda.device(device):
+        need = ctypes.c_size_t(0)
+        _check(getattr(_lib, name + "_workspace_size")(ctypes.byref(d), ctypes.byref(need)))
+        ws = _scratch(max(need.value, 1), workspace, device, stream)
+        _check(fn(ctypes.byref(d), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+@dataclass
+class PagedKV:
+    """Paged key-value cache of one receiver layer (include/mf.h, mf_paged_kv)."""
+    K: torch.Tensor            # [n_pages, page_size, h_kv, d], pages may be strided
+    V: torch.Tensor            # as K
+    block_table: torch.Tensor  # int32 [nseq, max_pages]
+    seq_lens: torch.Tensor     # int32 [nseq]
+    max_len: int               # host bound: every length <= max_len
+
+    @property
+    def nseq(self) -> int:
+        return self.block_table.shape[0]
+
+    @property
+    def h_kv(self) -> int:
+        return self.K.shape[2]
+
+    @property
+    def device(self):
+        return self.K.device
+
+    def desc(self) -> PagedKVDesc:
+        _dt(self.K)
+        _need(self.K, "K", self.K.dtype, (None,) * 4, contiguous=False)
+        _need(self.V, "V", self.K.dtype, tuple(self.K.shape), self.device, contiguous=False)
+        _need(self.block_table, "block_table", torch.int32, (None, None), self.device)
+        _need(self.seq_lens, "seq_lens", torch.int32, (self.nseq,), self.device)
+        stride = _row_stride(self.K, "K")
+        if _row_stride(self.V, "V") != stride:
+            raise ValueError("K and V must have the same page stride")
+        n_pages, page_size, h_kv, d = self.K.shape
+        return PagedKVDesc(_ptr(self.K), _ptr(self.V), _dt(self.K), stride, n_pages, page_size,
+                           self.block_table.shape[1], h_kv, d, _ptr(self.block_table),
+                           _ptr(self.seq_lens), self.nseq, int(self.max_len))
+
+
+def _score_pair(kv, a, b, dtype, what):
+    """Both arrays of a per-slot quantity: [nseq, h_kv, stride] with one stride."""
+    for t, w in ((a, what), (b, what + "_out")):
+        if t is not None:
+            _need(t, w, dtype, (kv.nseq, kv.h_kv, None if a is None else a.shape[2]), kv.device)
+
+
+def mf_paged_decode_workspace_size(kv: PagedKV, h_r: int, scores: bool = False) -> int:
+    d = PagedDecodeDesc()
+    d.kv, d.h_r = kv.desc(), int(h_r)
+    d.Q = d.O = 256  # only the shape is examined
+    if scores:
+        d.score_out, d.score_stride = 256, max(int(kv.max_len), 1)
+    n = ctypes.c_size_t(0)
+    _check(_lib.mf_paged_decode_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+    return n.value
+
+
+def mf_paged_decode(kv: PagedKV, Q: torch.Tensor, O: Optional[torch.Tensor] = None,
+                    scale: float = 0.0, lse: Optional[torch.Tensor] = None,
+                    score: Optional[torch.Tensor] = None, score_out: Optional[torch.Tensor] = None,
+                    o_f32: bool = False, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """Enqueue attention of one new token per sequence, Q [nseq, h_r, d] (rows may be strided),
+    over the cache; returns O [nseq, h_r, d] (allocated when None; float32 with o_f32).  scale 0
+    means 1 / sqrt(d).  lse: float32 [nseq, h_r] out.  score float32 [nseq, h_kv, stride]: the
+    call's weights are added to it, into score_out when given, else in place; score_out alone
+    receives the weights."""
+    kd = kv.desc()
+    dev = kv.device
+    _need(Q, "Q", kv.K.dtype, (kv.nseq, None, kv.K.shape[3]), dev, contiguous=False)
+    h_r = Q.shape[1]
+    if O is None:
+        O = torch.empty((kv.nseq, h_r, Q.shape[2]), dtype=torch.float32 if o_f32 else Q.dtype, device=dev)
+        if stream is not None:
+            O.record_stream(stream)
+    _need(O, "O", torch.float32 if o_f32 else Q.dtype, (kv.nseq, h_r, Q.shape[2]), dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (kv.nseq, h_r), dev)
+    _score_pair(kv, score, score_out, torch.float32, "score")
+    if score_out is None:
+        score_out = score
+    d = PagedDecodeDesc(kd, _ptr(Q), _row_stride(Q, "Q"), h_r, float(scale), _ptr(O), _ptr(lse),
+                        _ptr(score), _ptr(score_out), 0 if score_out is None else score_out.shape[2],
+                        MF_DECODE_O_F32 if o_f32 else 0)
+    _enqueue("mf_paged_decode", d, workspace, dev, stream)
+    return O
+
+
+def mf_kv_append(kv: PagedKV, K_new: torch.Tensor, V_new: torch.Tensor, cu_seqlens_new: torch.Tensor,
+                 max_new: int, n_seen: Optional[torch.Tensor] = None,
+                 score: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                 stream=None) -> None:
+    """Enqueue the copy of new tokens' K_new, V_new [T, h_kv, d] (rows may be strided) into the
+    cache, whose seq_lens already count them; their scores become 0 and their positions
+    n_seen - n .. n_seen - 1 where score / pos [nseq, h_kv, stride] are given."""
+    kd = kv.desc()
+    dev = kv.device
+    shape = (None, kv.h_kv, kv.K.shape[3])
+    _need(K_new, "K_new", kv.K.dtype, shape, dev, contiguous=False)
+    _need(V_new, "V_new", kv.K.dtype, tuple(K_new.shape), dev, contiguous=False)
+    _need(cu_seqlens_new, "cu_seqlens_new", torch.int32, (kv.nseq + 1,), dev)
+    stride = _row_stride(K_new, "K_new")
+    if _row_stride(V_new, "V_new") != stride:
+        raise ValueError("K_new and V_new must have the same row stride")
+    if n_seen is not None:
+        _need(n_seen, "n_seen", torch.int32, (kv.nseq,), dev)
+    wide = None
+    for t, what, dt in ((score, "score", torch.float32), (pos, "pos", torch.int32)):
+        if t is not None:
+            _need(t, what, dt, (kv.nseq, kv.h_kv, wide), dev)
+            wide = t.shape[2]
+    d = KvAppendDesc(kd, _ptr(K_new), _ptr(V_new), stride, K_new.shape[0], _ptr(cu_seqlens_new),
+                     int(max_new), _ptr(n_seen), _ptr(score), _ptr(pos), wide or 0)
+    with torch.cuda.device(dev):
+        _check(_lib.mf_kv_append(ctypes.byref(d), _stream(stream)))
+
+
+def mf_kv_evict_workspace_size(kv: PagedKV, budget: int) -> int:
+    d = KvEvictDesc()
+    d.kv, d.budget, d.score_stride = kv.desc(), int(budget), max(int(kv.max_len), 1)
+    d.score_in = d.pos_in = d.score_out = d.pos_out = d.seq_lens_out = 256
+    n = ctypes.c_size_t(0)
+    _check(_lib.mf_kv_evict_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+    return n.value
+
+
+def mf_kv_evict(kv: PagedKV, score: torch.Tensor, pos: torch.Tensor, budget: int, sink: int = 0,
+                window: int = 0, n_seen: Optional[torch.Tensor] = None,
+                score_out: Optional[torch.Tensor] = None, pos_out: Optional[torch.Tensor] = None,
+                seq_lens_out: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Enqueue the cut of every (sequence, key head) back to `budget` slots: positions below
+    `sink`, the last `window` positions (counted from n_seen) and the highest scores stay; kept
+    rows past the budget move into the dropped slots.  score float32 and pos int32
+    [nseq, h_kv, stride] follow, in place unless score_out / pos_out are given.  Returns the new
+    lengths: seq_lens_out, or kv.seq_lens updated in place."""
+    kd = kv.desc()
+    dev = kv.device
+    _score_pair(kv, score, score_out, torch.float32, "score")
+    _need(pos, "pos", torch.int32, tuple(score.shape), dev)
+    _score_pair(kv, pos, pos_out, torch.int32, "pos")
+    if n_seen is not None:
+        _need(n_seen, "n_seen", torch.int32, (kv.nseq,), dev)
+    out = kv.seq_lens if seq_lens_out is None else seq_lens_out
+    _need(out, "seq_lens_out", torch.int32, (kv.nseq,), dev)
+    d = KvEvictDesc(kd, _ptr(score), _ptr(pos), _ptr(score if score_out is None else score_out),
+                    _ptr(pos if pos_out is None else pos_out), score.shape[2], _ptr(n_seen),
+                    int(budget), int(sink), int(window), _ptr(out))
+    _enqueue("mf_kv_evict", d, workspace, dev, stream)
+    return out
+
+
+def mf_map_key_scores_workspace_size(capacity: int, B: int, h_kv: int) -> int:
+    d = KeyScoresDesc()
+    d.bsr = BsrDesc(256, 256, 256, int(capacity))
+    d.map_dtype, d.h_s, d.B, d.h_r, d.h_kv, d.nseq = MF_BF16, 1, int(B), int(h_kv), int(h_kv), 1
+    d.W = d.cu_seqlens = d.qblock_base = d.score = 256
+    d.score_stride = 1
+    n = ctypes.c_size_t(0)
+    _check(_lib.mf_map_key_scores_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+    return n.value
+
+
+def mf_map_key_scores(bsr: BSR, W: torch.Tensor, cu_seqlens: torch.Tensor, qblock_base: torch.Tensor,
+                      max_seqlen: int, h_kv: int, score: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Enqueue the weights that every key of every sequence gathered in a prefill over reused maps:
+    one receiver layer's W float32 [h_r, h_s], one sender layer's BSR.  Returns score float32
+    [nseq, h_kv, stride >= max_seqlen] (allocated as zeros when None); slots past a sequence's
+    length are left as they were."""
+    dev = bsr.values.device
+    _dt(bsr.values)
+    _need(bsr.values, "values", bsr.values.dtype, (None,) * 4, dev)
+    _need(bsr.row_ptr, "row_ptr", torch.int32, (None,), dev)
+    _need(bsr.col_idx, "col_idx", torch.int32, (None,), dev)
+    cap, h_s, B, B2 = bsr.values.shape
+    if B2 != B or bsr.col_idx.numel() < cap or bsr.row_ptr.numel() < 1:
+        raise ValueError("values must be [capacity, h_s, B, B], col_idx [capacity], row_ptr [rows + 1]")
+    _need(W, "W", torch.float32, (None, h_s), dev)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (None,), dev)
+    nseq = cu_seqlens.numel() - 1
+    _need(qblock_base, "qblock_base", torch.int32, (max(nseq, 0),), dev)
+    if score is None:
+        score = torch.zeros((nseq, h_kv, max(int(max_seqlen), 1)), dtype=torch.float32, device=dev)
+        if stream is not None:
+            score.record_stream(stream)
+    _need(score, "score", torch.float32, (nseq, h_kv, None), dev)
+    d = KeyScoresDesc(bsr.desc(), bsr.row_ptr.numel() - 1, _dt(bsr.values), h_s, B, _ptr(W),
+                      W.shape[0], int(h_kv), _ptr(cu_seqlens), _ptr(qblock_base), nseq,
+                      int(max_seqlen), _ptr(score), score.shape[2])
+    _enqueue("mf_map_key_scores", d, workspace, dev, stream)
+    return score

@@ -219,6 +219,120 @@ mf_status check_calib(const mf_calib_desc* d) {
     return fail(MF_ERR_INVALID, "maps must be 16-byte aligned");
   return MF_OK;
 }
+
+bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+// a stride in elements: 0 (the dense one) or at least `least`, whole 16-byte vectors
+bool bad_stride(int64_t stride, int64_t least, int64_t elem) {
+  return stride != 0 && (stride < least || stride > ((int64_t)1 << 56) || (stride * elem) % 16);
+}
+
+mf_status check_kv(const mf_paged_kv& k) {
+  if (!k.K || !k.V || !k.block_table || !k.seq_lens) return fail(MF_ERR_INVALID, "a required cache pointer is NULL");
+  if (!is_dtype(k.dtype)) return fail(MF_ERR_INVALID, "cache dtype must be MF_F32 or MF_BF16");
+  if (k.n_pages < 1 || k.page_size < 1 || k.max_pages < 1) return fail(MF_ERR_INVALID, "n_pages, page_size and max_pages must be >= 1");
+  if (k.nseq < 1 || k.max_len < 0) return fail(MF_ERR_INVALID, "nseq must be >= 1 and max_len >= 0");
+  if (k.h_kv < 1 || k.d < 1) return fail(MF_ERR_INVALID, "h_kv and d must be >= 1");
+  if (k.nseq > 4096) return fail(MF_ERR_UNSUPPORTED, "more than 4096 sequences");
+  if ((int64_t)k.nseq * k.max_len >= (int64_t)1 << 31) return fail(MF_ERR_UNSUPPORTED, "nseq * max_len must be below 2^31");
+  if (k.h_kv > 64) return fail(MF_ERR_UNSUPPORTED, "h_kv must be <= 64");
+  if (k.d % 8 || k.d > 256) return fail(MF_ERR_UNSUPPORTED, "d must be a multiple of 8, at most 256");
+  const int64_t e = k.dtype == MF_F32 ? 4 : 2;
+  if (bad_stride(k.page_stride, (int64_t)k.page_size * k.h_kv * k.d, e))
+    return fail(MF_ERR_INVALID, "page_stride must be 0, or cover a page in a multiple of 16 bytes");
+  if (misaligned(k.K, 16) || misaligned(k.V, 16)) return fail(MF_ERR_INVALID, "K and V must be 16-byte aligned");
+  if (misaligned(k.block_table, 4) || misaligned(k.seq_lens, 4)) return fail(MF_ERR_INVALID, "block_table and seq_lens must be 4-byte aligned");
+  return MF_OK;
+}
+
+mf_status check_score_stride(const mf_paged_kv& k, int64_t stride) {
+  if (stride < k.max_len || stride < 1) return fail(MF_ERR_INVALID, "score_stride must be >= max_len and >= 1");
+  if (stride > (int64_t)1 << 40) return fail(MF_ERR_UNSUPPORTED, "score_stride too large");
+  return MF_OK;
+}
+
+mf_status check_paged_decode(const mf_paged_decode_desc* d) {
+  if (!d) return fail(MF_ERR_INVALID, "desc is NULL");
+  mf_status s = check_kv(d->kv);
+  if (s != MF_OK) return s;
+  if (!d->Q || !d->O) return fail(MF_ERR_INVALID, "Q or O is NULL");
+  if (d->h_r < 1 || d->h_r % d->kv.h_kv) return fail(MF_ERR_INVALID, "h_r must be a multiple of h_kv");
+  if (d->h_r > 256) return fail(MF_ERR_UNSUPPORTED, "h_r must be <= 256");
+  if (!(d->scale >= 0.0f) || std::isinf(d->scale)) return fail(MF_ERR_INVALID, "scale must be finite and >= 0");
+  if (d->flags & ~MF_DECODE_O_F32) return fail(MF_ERR_INVALID, "unknown decode flags");
+  if (bad_stride(d->q_stride, (int64_t)d->h_r * d->kv.d, d->kv.dtype == MF_F32 ? 4 : 2))
+    return fail(MF_ERR_INVALID, "q_stride must be 0, or cover a row in a multiple of 16 bytes");
+  if (misaligned(d->Q, 16) || misaligned(d->O, 16)) return fail(MF_ERR_INVALID, "Q and O must be 16-byte aligned");
+  if (misaligned(d->lse, 4) || misaligned(d->score_in, 4) || misaligned(d->score_out, 4))
+    return fail(MF_ERR_INVALID, "lse and scores must be 4-byte aligned");
+  if (d->score_in && !d->score_out) return fail(MF_ERR_INVALID, "score_in without score_out");
+  return d->score_out ? check_score_stride(d->kv, d->score_stride) : MF_OK;
+}
+
+mf_status check_kv_append(const mf_kv_append_desc* d) {
+  if (!d) return fail(MF_ERR_INVALID, "desc is NULL");
+  mf_status s = check_kv(d->kv);
+  if (s != MF_OK) return s;
+  if (!d->cu_seqlens_new || (d->total_new > 0 && (!d->K_new || !d->V_new)))
+    return fail(MF_ERR_INVALID, "K_new, V_new or cu_seqlens_new is NULL");
+  if (d->total_new < 0 || d->max_new < 0 || d->max_new > d->kv.max_len)
+    return fail(MF_ERR_INVALID, "total_new must be >= 0 and max_new in [0, max_len]");
+  if (bad_stride(d->new_stride, (int64_t)d->kv.h_kv * d->kv.d, d->kv.dtype == MF_F32 ? 4 : 2))
+    return fail(MF_ERR_INVALID, "new_stride must be 0, or cover a row in a multiple of 16 bytes");
+  if (misaligned(d->K_new, 16) || misaligned(d->V_new, 16)) return fail(MF_ERR_INVALID, "K_new and V_new must be 16-byte aligned");
+  if (misaligned(d->cu_seqlens_new, 4) || misaligned(d->n_seen, 4) || misaligned(d->score, 4) || misaligned(d->pos, 4))
+    return fail(MF_ERR_INVALID, "index, score and position arrays must be 4-byte aligned");
+  return d->score || d->pos ? check_score_stride(d->kv, d->score_stride) : MF_OK;
+}
+
+mf_status check_kv_evict(const mf_kv_evict_desc* d) {
+  if (!d) return fail(MF_ERR_INVALID, "desc is NULL");
+  mf_status s = check_kv(d->kv);
+  if (s != MF_OK) return s;
+  if (!d->score_in || !d->pos_in || !d->score_out || !d->pos_out || !d->seq_lens_out)
+    return fail(MF_ERR_INVALID, "a score, position or length pointer is NULL");
+  if (misaligned(d->score_in, 4) || misaligned(d->pos_in, 4) || misaligned(d->score_out, 4) ||
+      misaligned(d->pos_out, 4) || misaligned(d->n_seen, 4) || misaligned(d->seq_lens_out, 4))
+    return fail(MF_ERR_INVALID, "score, position and length arrays must be 4-byte aligned");
+  if (d->budget < 1 || d->sink < 0 || d->window < 0 || (int64_t)d->sink + d->window > d->budget)
+    return fail(MF_ERR_INVALID, "budget must be >= 1 and cover sink + window");
+  return check_score_stride(d->kv, d->score_stride);
+}
+
+mf_status check_key_scores(const mf_key_scores_desc* d) {
+  if (!d) return fail(MF_ERR_INVALID, "desc is NULL");
+  if (!is_dtype(d->map_dtype)) return fail(MF_ERR_INVALID, "map_dtype must be MF_F32 or MF_BF16");
+  if (!d->bsr.row_ptr || !d->W || !d->cu_seqlens || !d->qblock_base || !d->score ||
+      (d->bsr.capacity_blocks > 0 && (!d->bsr.col_idx || !d->bsr.values)))
+    return fail(MF_ERR_INVALID, "a required pointer is NULL");
+  if (!(d->B == 32 || d->B == 64 || d->B == 128)) return fail(MF_ERR_INVALID, "B must be 32, 64 or 128");
+  if (d->h_s < 1 || d->h_s > 256) return fail(MF_ERR_INVALID, "h_s must be in [1, 256]");
+  if (d->h_kv < 1 || d->h_r < 1 || d->h_r % d->h_kv) return fail(MF_ERR_INVALID, "h_r must be a multiple of h_kv");
+  if (d->h_kv > 64 || d->h_r > 256) return fail(MF_ERR_UNSUPPORTED, "h_kv must be <= 64 and h_r <= 256");
+  if (d->nseq < 1 || d->max_seqlen < 0) return fail(MF_ERR_INVALID, "nseq must be >= 1 and max_seqlen >= 0");
+  if (d->nseq > 4096) return fail(MF_ERR_UNSUPPORTED, "more than 4096 sequences");
+  if (((int64_t)d->max_seqlen + d->B - 1) / d->B > 4096) return fail(MF_ERR_UNSUPPORTED, "more than 4096 query blocks per sequence");
+  if (d->n_rows < 0 || d->n_rows >= (int64_t)1 << 24) return fail(MF_ERR_INVALID, "n_rows must be in [0, 2^24)");
+  if (d->bsr.capacity_blocks < 0 || d->bsr.capacity_blocks >= (int64_t)1 << 31) return fail(MF_ERR_INVALID, "bad capacity_blocks");
+  if (d->score_stride < d->max_seqlen || d->score_stride < 1 || d->score_stride > (int64_t)1 << 40)
+    return fail(MF_ERR_INVALID, "score_stride must be >= max_seqlen and >= 1");
+  if (misaligned(d->bsr.values, 16)) return fail(MF_ERR_INVALID, "values must be 16-byte aligned");
+  if (misaligned(d->W, 4) || misaligned(d->score, 4) || misaligned(d->cu_seqlens, 4) ||
+      misaligned(d->qblock_base, 4) || misaligned(d->bsr.row_ptr, 4) || misaligned(d->bsr.col_idx, 4))
+    return fail(MF_ERR_INVALID, "index arrays, W and score must be 4-byte aligned");
+  return MF_OK;
+}
+
+mf_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (!ws || have < need) return fail(MF_ERR_INVALID, "workspace missing or smaller than the size this descriptor needs");
+  if (misaligned(ws, 256)) return fail(MF_ERR_INVALID, "workspace must be 256-byte aligned");
+  return MF_OK;
+}
+
+mf_status launched(const char* what, cudaError_t e) {
+  if (e == cudaSuccess) return MF_OK;
+  return fail(MF_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
+}
 }  // namespace
 
 extern "C" {
@@ -235,6 +349,10 @@ size_t mf_abi_struct_size(int which) {
     case 2: return sizeof(mf_retrieve_desc);
     case 3: return sizeof(mf_calib_desc);
     case 4: return sizeof(mf_compress_qk_desc);
+    case 5: return sizeof(mf_paged_decode_desc);
+    case 6: return sizeof(mf_kv_append_desc);
+    case 8: return sizeof(mf_kv_evict_desc);
+    case 9: return sizeof(mf_key_scores_desc);
     default: return 0;
   }
 }
@@ -505,6 +623,74 @@ mf_status mf_calib_solve(const double* gram, int h_s, int h_r, double ridge, flo
                                           static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(MF_ERR_CUDA, std::string("calib solve launch: ") + cudaGetErrorString(e));
   return MF_OK;
+}
+
+mf_status mf_paged_decode_workspace_size(const mf_paged_decode_desc* desc, size_t* bytes) {
+  if (!bytes) return fail(MF_ERR_INVALID, "bytes is NULL");
+  mf_status s = check_paged_decode(desc);
+  if (s != MF_OK) return s;
+  *bytes = mfi::paged_decode_ws(*desc, nullptr, nullptr);
+  return MF_OK;
+}
+
+mf_status mf_paged_decode(const mf_paged_decode_desc* desc, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  mf_status s = check_paged_decode(desc);
+  if (s == MF_OK) s = check_workspace(workspace, workspace_bytes, mfi::paged_decode_ws(*desc, nullptr, nullptr));
+  if (s != MF_OK) return s;
+  uint32_t* st = status_ptr();
+  if (!st) return fail(MF_ERR_CUDA, "cannot resolve the device status word");
+  mfi::PagedDecodeWs ws;
+  mfi::paged_decode_ws(*desc, &ws, workspace);
+  return launched("mf_paged_decode", mfi::launch_paged_decode(*desc, ws, st, static_cast<cudaStream_t>(stream)));
+}
+
+mf_status mf_kv_append(const mf_kv_append_desc* desc, void* stream) {
+  mf_status s = check_kv_append(desc);
+  if (s != MF_OK) return s;
+  uint32_t* st = status_ptr();
+  if (!st) return fail(MF_ERR_CUDA, "cannot resolve the device status word");
+  return launched("mf_kv_append", mfi::launch_kv_append(*desc, st, static_cast<cudaStream_t>(stream)));
+}
+
+mf_status mf_kv_evict_workspace_size(const mf_kv_evict_desc* desc, size_t* bytes) {
+  if (!bytes) return fail(MF_ERR_INVALID, "bytes is NULL");
+  mf_status s = check_kv_evict(desc);
+  if (s != MF_OK) return s;
+  *bytes = mfi::kv_evict_ws(*desc, nullptr, nullptr);
+  return MF_OK;
+}
+
+mf_status mf_kv_evict(const mf_kv_evict_desc* desc, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  mf_status s = check_kv_evict(desc);
+  if (s == MF_OK) s = check_workspace(workspace, workspace_bytes, mfi::kv_evict_ws(*desc, nullptr, nullptr));
+  if (s != MF_OK) return s;
+  uint32_t* st = status_ptr();
+  if (!st) return fail(MF_ERR_CUDA, "cannot resolve the device status word");
+  mfi::KvEvictWs ws;
+  mfi::kv_evict_ws(*desc, &ws, workspace);
+  return launched("mf_kv_evict", mfi::launch_kv_evict(*desc, ws, st, static_cast<cudaStream_t>(stream)));
+}
+
+mf_status mf_map_key_scores_workspace_size(const mf_key_scores_desc* desc, size_t* bytes) {
+  if (!bytes) return fail(MF_ERR_INVALID, "bytes is NULL");
+  mf_status s = check_key_scores(desc);
+  if (s != MF_OK) return s;
+  *bytes = mfi::key_scores_ws(*desc, nullptr, nullptr);
+  return MF_OK;
+}
+
+mf_status mf_map_key_scores(const mf_key_scores_desc* desc, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  mf_status s = check_key_scores(desc);
+  if (s == MF_OK) s = check_workspace(workspace, workspace_bytes, mfi::key_scores_ws(*desc, nullptr, nullptr));
+  if (s != MF_OK) return s;
+  uint32_t* st = status_ptr();
+  if (!st) return fail(MF_ERR_CUDA, "cannot resolve the device status word");
+  mfi::KeyScoresWs ws;
+  mfi::key_scores_ws(*desc, &ws, workspace);
+  return launched("mf_map_key_scores", mfi::launch_key_scores(*desc, ws, st, static_cast<cudaStream_t>(stream)));
 }
 
 mf_status mf_set_wait_limit(uint64_t limit_ns, int stall) {

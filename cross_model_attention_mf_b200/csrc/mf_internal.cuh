@@ -105,4 +105,39 @@ bool launch_calib_gram(const mf_calib_desc& d, void* ws, uint32_t* status, cudaS
 cudaError_t launch_calib_solve(const double* gram, int h_s, int h_r, double ridge, float* W,
                                double* residual, uint32_t* status, cudaStream_t st);
 
+// single-token attention over the paged cache: scratch carved out of the caller's workspace
+struct PagedDecodeWs {
+  int32_t* pre;     // [nseq + 1] tiles before each sequence
+  float* lse2;      // [nseq][h_r]
+  float* part_O;    // parts of the units cut between CTAs
+  float2* part_ml;
+  float* S;         // x_j of every query head and key (with score_out)
+};
+size_t paged_decode_ws(const mf_paged_decode_desc& d, PagedDecodeWs* ws, void* base);
+cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecodeWs& ws,
+                                uint32_t* status, cudaStream_t st);
+
+cudaError_t launch_kv_append(const mf_kv_append_desc& d, uint32_t* status, cudaStream_t st);
+
+// eviction: the rows to move, per (sequence, key head)
+struct KvEvictWs {
+  int32_t* count;   // [nseq][h_kv] rows to move
+  int32_t* len;     // [nseq] new lengths
+  int32_t* dst;     // [nseq][h_kv][moves]
+  int32_t* src;
+  int64_t moves;    // most rows that one (sequence, key head) can move
+};
+size_t kv_evict_ws(const mf_kv_evict_desc& d, KvEvictWs* ws, void* base);
+cudaError_t launch_kv_evict(const mf_kv_evict_desc& d, const KvEvictWs& ws, uint32_t* status,
+                            cudaStream_t st);
+
+// weights gathered in a prefill: [slots][h_kv][B] column sums of mixed blocks, one slot per
+// stretch of blocks that a CTA shares with no other
+struct KeyScoresWs {
+  float* part;
+};
+size_t key_scores_ws(const mf_key_scores_desc& d, KeyScoresWs* ws, void* base);
+cudaError_t launch_key_scores(const mf_key_scores_desc& d, const KeyScoresWs& ws, uint32_t* status,
+                              cudaStream_t st);
+
 }  // namespace mfi

@@ -1,0 +1,798 @@
+// Attention of one new token per sequence over the paged key-value cache (mf_paged_decode).
+//
+//   x_j = c2 q.K[j] (c2 = scale log2 e),  m = max x_j,  l = sum 2^(x_j - m),
+//   O = sum 2^(x_j - m) V[j] / l,  lse = (m + log2 l) ln 2,
+// with (m, l, O) of two sets of keys joined by 2^(m_a - m), 2^(m_b - m).  K and V are read once:
+// 4 len h_r d operations on 2 len h_kv d elements, so HBM bandwidth bounds the call at any
+// group size the tensor cores serve.
+//
+// Split.  A unit is (sequence, key head, block of up to HT query heads of its group); the units
+// of the batch, cut into tiles of TK keys, lie one after another on a line that the CTAs share
+// evenly: whatever the lengths, every CTA gets the same number of tiles.  A CTA walks the units
+// of its stretch; a unit that lies wholly inside is finished there, a unit cut by a stretch's end
+// leaves (m, l, O) in the workspace, at most two per CTA, and k_decode_join adds the parts in
+// order.  Within a CTA the four warps take tiles in turn, each with its own ring of asynchronous
+// copies and its own (m, l, O): no CTA barrier inside a unit.
+//
+// Gathered weights need the final lse, so the main kernel stores x_j (4 bytes per query head and
+// key, against 2 d elements per key head) and the join kernel turns them into weights.
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "paged_kv.cuh"
+
+namespace mfi {
+namespace {
+
+constexpr int WARPS = 4;
+constexpr int NTHR = 32 * WARPS;
+constexpr int MAX_GRID = 512;     // CTAs of the main kernel (two partial results each)
+constexpr int MIN_TILES = WARPS;  // tiles a CTA takes at least: one per warp
+constexpr int JOIN_THR = 256;
+constexpr int JOIN_KEYS = 2048;   // keys per CTA of the join kernel
+constexpr float LN2 = 0.693147180559945309f;
+
+struct DecodeParams {
+  KvView kv;
+  const char* Q;
+  int64_t q_bytes;     // between the rows of two sequences
+  int h_r, h_kv, G, GP, hb, U, d;
+  float c2;
+  char* O;
+  int o_f32;
+  float* lse;          // or null
+  float* S;            // [nseq][h_kv][max_len][GP] x_j, or null
+  const float* score_in;
+  float* score_out;    // or null
+  int64_t score_stride;
+  int32_t* pre;        // [nseq + 1] tiles before each sequence
+  float* lse2;         // [nseq][h_r] of the units finished by one CTA
+  float* part_O;       // [2 grid][HT][d]
+  float2* part_ml;     // [2 grid][HT]
+  int grid;
+  int whole;           // every unit is finished by one CTA
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+// 16 bytes to shared memory, zeros when bytes == 0
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 8x8 transpose of 16-bit values across the warp
+__device__ __forceinline__ uint32_t mov_trans(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// one warp's share of a unit
+struct Unit {
+  int s, hk, h0, nh, len;  // sequence, key head, first query head, heads, sequence length
+  int t0, t1;              // tiles [t0, t1) of the unit belong to this CTA
+};
+
+// What the two cores (bf16 on the tensor cores, float32 on the FMA pipes) share: TK keys per
+// tile, HT query heads per unit, DP the padded head dim, STAGES tiles in a warp's ring.
+// run() leaves the warp's m, l in sm / sl [HT] and its O in buf [HT][DP + PAD].
+
+template <int DP_, int NT>
+struct CoreBf16 {
+  static constexpr int DP = DP_, TK = 16, HT = 8 * NT, ESZ = 2;
+  static constexpr int CPR = DP / 8;                 // 16-byte chunks per row
+  static constexpr int TILE = 2 * TK * DP * ESZ;     // K rows, then V rows
+  static constexpr int STAGES = DP == 64 ? 6 : DP == 128 ? 3 : DP == 192 ? 2 : 3;
+  static constexpr int CTAS = DP == 256 ? 1 : 2;
+  static constexpr int LDB = DP + 4;                 // conflict-free writes of the fragments
+  static constexpr int Q_FLOATS = 0;
+  static_assert(HT * LDB * 4 <= STAGES * TILE, "O fits the warp's ring");
+
+  __device__ static void run(const DecodeParams& p, const Unit& u, uint8_t* ring, float*, float* sm,
+                             float* sl, int warp, int lane) {
+    const KvView& kv = p.kv;
+    const int g = lane >> 2, t = lane & 3;
+    const int nch = p.d >> 3;
+    // Q^T fragments: head g (+ 8 per head tile), dims 16 k + 2 t (+ 8)
+    uint32_t q[DP / 16][NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int h = g + 8 * n;
+      const char* qr = p.Q + (int64_t)u.s * p.q_bytes + (int64_t)(u.h0 + h) * p.d * 2;
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int c = 16 * k + 2 * t + 8 * j;
+          q[k][n][j] = h < u.nh && c < p.d ? *reinterpret_cast<const uint32_t*>(qr + 2 * c) : 0u;
+        }
+    }
+    float o[DP / 16][NT][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[k][n][j] = 0.0f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+    }
+    const int first = u.t0 + warp;
+    const int n_my = first < u.t1 ? (u.t1 - first + WARPS - 1) / WARPS : 0;
+    const uint32_t sring = smem_u32(ring);
+    const int64_t hoff = (int64_t)u.hk * kv.row_bytes;
+    // byte offset of key row `lane` (< 16) of the k-th tile, -1 past the end
+    auto rows_of = [&](int k) -> int64_t {
+      const int key = (first + k * WARPS) * TK + (lane & 15);
+      if (k >= n_my || key >= u.len) return -1;
+      return kv_slot(kv, u.s, key);
+    };
+    auto issue = [&](int stage, int64_t off) {
+      const uint32_t base = sring + stage * TILE;
+#pragma unroll
+      for (int i = 0; i < CPR / 2; ++i) {
+        const int idx = i * 32 + lane;
+        const int row = idx / CPR, c = idx % CPR;
+        const int64_t ro = __shfl_sync(~0u, off, row);
+        const bool ok = ro >= 0 && c < nch;
+        const int64_t a = ok ? ro + hoff + c * 16 : 0;
+        const uint32_t dst = base + (row * CPR + (c ^ (row & 7))) * 16;
+        cp16(dst, kv.K + a, ok ? 16u : 0u);
+        cp16(dst + TK * DP * ESZ, kv.V + a, ok ? 16u : 0u);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < STAGES - 1; ++k) {
+      if (k < n_my) issue(k, rows_of(k));
+      cp_commit();
+    }
+    int64_t next = rows_of(STAGES - 1);
+    int stage = 0, fill = STAGES - 1;
+    float* S = p.S ? p.S + ((int64_t)u.s * p.h_kv + u.hk) * kv.max_len * p.GP : nullptr;
+    const int hg = u.h0 - u.hk * p.G;  // first head within the group
+    for (int k = 0; k < n_my; ++k) {
+      cp_wait<STAGES - 2>();
+      __syncwarp();
+      if (k + STAGES - 1 < n_my) issue(fill, next);
+      cp_commit();
+      next = rows_of(k + STAGES);
+      const uint32_t kb = sring + stage * TILE, vb = kb + TK * DP * ESZ;
+      if (++stage == STAGES) stage = 0;
+      if (++fill == STAGES) fill = 0;
+
+      // S^T[key][head]: rows g and g + 8, heads 2t, 2t + 1; two chains of accumulators
+      float sc[2][NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[0][n][j] = sc[1][n][j] = 0.0f;
+      {
+        const int row = lane & 15, hi = lane >> 4;
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) {
+          uint32_t a[4];
+          ldm4(a, kb + (row * CPR + ((2 * ks + hi) ^ (row & 7))) * 16);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(sc[ks & 1][n], a, q[ks][n][0], q[ks][n][1]);
+        }
+      }
+      const int key = (first + k * WARPS) * TK + g;
+      const bool in0 = key < u.len, in1 = key + 8 < u.len;
+      uint32_t phi[NT][2], plo[NT][2];
+      bool moved = false;
+      float al[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = (sc[0][n][j] + sc[1][n][j]) * p.c2;
+        if (!in0) x[0] = x[1] = -INFINITY;
+        if (!in1) x[2] = x[3] = -INFINITY;
+        if (S) {
+          const int h = 8 * n + 2 * t;
+          if (h < u.nh) {  // GP is even: the pair stays inside the key's row
+            if (in0) *reinterpret_cast<float2*>(S + (int64_t)key * p.GP + hg + h) = make_float2(x[0], x[1]);
+            if (in1) *reinterpret_cast<float2*>(S + (int64_t)(key + 8) * p.GP + hg + h) = make_float2(x[2], x[3]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float mx = fmaxf(x[j], x[j + 2]);
+          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+          const float mn = fmaxf(m[n][j], mx);
+          const float mu = mn == -INFINITY ? 0.0f : mn;
+          al[n][j] = ex2(m[n][j] - mu);
+          moved |= mn != m[n][j];
+          m[n][j] = mn;
+          x[j] = ex2(x[j] - mu);
+          x[j + 2] = ex2(x[j + 2] - mu);
+          l[n][j] = l[n][j] * al[n][j] + (x[j] + x[j + 2]);
+        }
+        // weights as a bf16 pair, transposed into the B operand: head g, keys 2t, 2t + 1 (+ 8)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float a = x[2 * j], b = x[2 * j + 1];
+          const uint32_t hi = pack_bf16(a, b);
+          const float ah = __uint_as_float(hi << 16), bh = __uint_as_float(hi & 0xFFFF0000u);
+          phi[n][j] = mov_trans(hi);
+          plo[n][j] = mov_trans(pack_bf16(a - ah, b - bh));
+        }
+      }
+      if (__any_sync(~0u, moved)) {
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            o[i][n][0] *= al[n][0];
+            o[i][n][1] *= al[n][1];
+            o[i][n][2] *= al[n][0];
+            o[i][n][3] *= al[n][1];
+          }
+      }
+      // O^T[dim][head] += V^T P^T
+      {
+        const int row = (lane & 7) + 8 * (lane >> 4), hi = (lane >> 3) & 1;
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) {
+          uint32_t a[4];
+          ldm4t(a, vb + (row * CPR + ((2 * i + hi) ^ (row & 7))) * 16);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816(o[i][n], a, phi[n][0], phi[n][1]);
+            mma16816(o[i][n], a, plo[n][0], plo[n][1]);
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+    __syncwarp();
+    float* buf = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float v = l[n][j];
+        v += __shfl_xor_sync(~0u, v, 4);
+        v += __shfl_xor_sync(~0u, v, 8);
+        v += __shfl_xor_sync(~0u, v, 16);
+        if (g == 0) {
+          sm[8 * n + 2 * t + j] = m[n][j];
+          sl[8 * n + 2 * t + j] = v;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          buf[(8 * n + 2 * t + (j & 1)) * LDB + 16 * i + g + 8 * (j >> 1)] = o[i][n][j];
+    }
+  }
+};
+
+template <int DP_>
+struct CoreF32 {
+  static constexpr int DP = DP_, TK = 8, HT = 8, ESZ = 4;
+  static constexpr int CPR = DP / 4;
+  static constexpr int TILE = 2 * TK * DP * ESZ;
+  static constexpr int STAGES = DP == 64 ? 6 : DP == 128 ? 3 : DP == 192 ? 2 : 3;
+  static constexpr int CTAS = DP == 256 ? 1 : 2;
+  static constexpr int LDB = DP;
+  static constexpr int Q_FLOATS = HT * DP;
+  static constexpr int NV = (CPR + 31) / 32;         // 16-byte chunks of a row per lane
+  static_assert(HT * LDB * 4 <= STAGES * TILE, "O fits the warp's ring");
+
+  __device__ static void run(const DecodeParams& p, const Unit& u, uint8_t* ring, float* sq, float* sm,
+                             float* sl, int warp, int lane) {
+    const KvView& kv = p.kv;
+    const int nch = p.d >> 2;
+    __syncthreads();  // the previous unit's reads of sq are done
+    for (int i = threadIdx.x; i < HT * DP; i += NTHR) {
+      const int h = i / DP, c = i % DP;
+      sq[i] = h < u.nh && c < p.d ? reinterpret_cast<const float*>(p.Q + (int64_t)u.s * p.q_bytes)[(int64_t)(u.h0 + h) * p.d + c] : 0.0f;
+    }
+    __syncthreads();
+    float4 o[HT][NV];
+    float m[HT], l[HT];
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) o[h][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      m[h] = -INFINITY;
+      l[h] = 0.0f;
+    }
+    const int first = u.t0 + warp;
+    const int n_my = first < u.t1 ? (u.t1 - first + WARPS - 1) / WARPS : 0;
+    const uint32_t sring = smem_u32(ring);
+    const int64_t hoff = (int64_t)u.hk * kv.row_bytes;
+    auto rows_of = [&](int k) -> int64_t {
+      const int key = (first + k * WARPS) * TK + (lane & 7);
+      if (k >= n_my || key >= u.len) return -1;
+      return kv_slot(kv, u.s, key);
+    };
+    auto issue = [&](int stage, int64_t off) {
+      const uint32_t base = sring + stage * TILE;
+#pragma unroll
+      for (int i = 0; i < CPR / 4; ++i) {
+        const int idx = i * 32 + lane;
+        const int row = idx / CPR, c = idx % CPR;
+        const int64_t ro = __shfl_sync(~0u, off, row);
+        const bool ok = ro >= 0 && c < nch;
+        const int64_t a = ok ? ro + hoff + c * 16 : 0;
+        const uint32_t dst = base + (row * CPR + (c ^ row)) * 16;
+        cp16(dst, kv.K + a, ok ? 16u : 0u);
+        cp16(dst + TK * DP * ESZ, kv.V + a, ok ? 16u : 0u);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < STAGES - 1; ++k) {
+      if (k < n_my) issue(k, rows_of(k));
+      cp_commit();
+    }
+    int64_t next = rows_of(STAGES - 1);
+    int stage = 0, fill = STAGES - 1;
+    float* S = p.S ? p.S + ((int64_t)u.s * p.h_kv + u.hk) * kv.max_len * p.GP : nullptr;
+    const int hg = u.h0 - u.hk * p.G;
+    const int kl = lane & 7, part = lane >> 3;
+    for (int k = 0; k < n_my; ++k) {
+      cp_wait<STAGES - 2>();
+      __syncwarp();
+      if (k + STAGES - 1 < n_my) issue(fill, next);
+      cp_commit();
+      next = rows_of(k + STAGES);
+      const float4* Kt = reinterpret_cast<const float4*>(ring + stage * TILE);
+      const float4* Vt = Kt + TK * CPR;
+      if (++stage == STAGES) stage = 0;
+      if (++fill == STAGES) fill = 0;
+      // lane (key kl, part): every fourth 16-byte chunk of the key's row, all heads
+      float x[HT];
+#pragma unroll
+      for (int h = 0; h < HT; ++h) x[h] = 0.0f;
+#pragma unroll 4
+      for (int c = part; c < CPR; c += 4) {
+        const float4 kk = Kt[kl * CPR + (c ^ kl)];
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+          const float4 qq = reinterpret_cast<const float4*>(sq)[h * CPR + c];
+          x[h] = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, fmaf(kk.w, qq.w, x[h]))));
+        }
+      }
+      const int key = (first + k * WARPS) * TK + kl;
+      const bool in = key < u.len;
+#pragma unroll
+      for (int h = 0; h < HT; ++h) {
+        float v = x[h];
+        v += __shfl_xor_sync(~0u, v, 8);
+        v += __shfl_xor_sync(~0u, v, 16);
+        v = in ? v * p.c2 : -INFINITY;
+        if (S && in && part == 0 && h < u.nh) S[(int64_t)key * p.GP + hg + h] = v;
+        float mx = v;
+        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+        const float mn = fmaxf(m[h], mx);
+        const float mu = mn == -INFINITY ? 0.0f : mn;
+        const float al = ex2(m[h] - mu);
+        m[h] = mn;
+        x[h] = ex2(v - mu);
+        l[h] = l[h] * al + x[h];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          o[h][i].x *= al;
+          o[h][i].y *= al;
+          o[h][i].z *= al;
+          o[h][i].w *= al;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < TK; ++j) {
+        float4 v[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = lane + 32 * i;
+          v[i] = c < CPR ? Vt[j * CPR + (c ^ j)] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+          const float w = __shfl_sync(~0u, x[h], j);
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            o[h][i].x = fmaf(w, v[i].x, o[h][i].x);
+            o[h][i].y = fmaf(w, v[i].y, o[h][i].y);
+            o[h][i].z = fmaf(w, v[i].z, o[h][i].z);
+            o[h][i].w = fmaf(w, v[i].w, o[h][i].w);
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+    __syncwarp();
+    float4* buf = reinterpret_cast<float4*>(ring);
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+      float v = l[h];
+      v += __shfl_xor_sync(~0u, v, 1);
+      v += __shfl_xor_sync(~0u, v, 2);
+      v += __shfl_xor_sync(~0u, v, 4);
+      if (lane == 0) {
+        sm[h] = m[h];
+        sl[h] = v;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = lane + 32 * i;
+        if (c < CPR) buf[h * (LDB / 4) + c] = o[h][i];
+      }
+    }
+  }
+};
+
+// tiles before each sequence, in shared memory; a sequence of length 0 takes one (empty) tile, so
+// that its outputs are written like any other's
+__device__ inline void scan_tiles(const KvView& kv, int tk, int32_t* pre, bool report) {
+  __shared__ int s_w[WARPS];
+  int base = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int s0 = 0; s0 < kv.nseq; s0 += NTHR) {
+    const int s = s0 + threadIdx.x;
+    int n = 0;
+    if (s < kv.nseq) n = max(1, (kv_len(kv, s, report) + tk - 1) / tk);
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(~0u, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_w[warp] = x;
+    __syncthreads();
+    int add = base, tot = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) add += s_w[w];
+      tot += s_w[w];
+    }
+    if (s < kv.nseq) pre[s] = add + x - n;
+    base += tot;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) pre[kv.nseq] = base;
+  __syncthreads();
+}
+
+__device__ __forceinline__ int64_t tiles_per_cta(int64_t total, int grid) {
+  const int64_t per = (total + grid - 1) / grid;
+  return per < MIN_TILES ? MIN_TILES : per;
+}
+
+template <class Core>
+__global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_constant__ DecodeParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_m[WARPS][Core::HT], s_l[WARPS][Core::HT];
+  constexpr int RING = Core::STAGES * Core::TILE;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = smem + warp * RING;
+  float* sq = reinterpret_cast<float*>(smem + WARPS * RING);
+  int32_t* pre = reinterpret_cast<int32_t*>(sq + Core::Q_FLOATS);
+
+  // the join kernel may take its place now; it waits for this grid before its first access
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int64_t x, end;
+  int s = 0;
+  if (p.whole) {
+    // one unit per CTA: nothing to share out
+    x = blockIdx.x;
+    end = x + 1;
+    s = (int)(x / p.U);
+  } else {
+    scan_tiles(p.kv, Core::TK, pre, blockIdx.x == 0);
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i <= p.kv.nseq; i += NTHR) p.pre[i] = pre[i];
+    const int64_t total = (int64_t)pre[p.kv.nseq] * p.U;
+    const int64_t per = tiles_per_cta(total, p.grid);
+    x = per * blockIdx.x;
+    end = min(total, x + per);
+    int hi = p.kv.nseq;  // the sequence whose stretch holds x
+    while (hi - s > 1) {
+      const int mid = (s + hi) >> 1;
+      if ((int64_t)pre[mid] * p.U <= x) s = mid; else hi = mid;
+    }
+  }
+  while (x < end) {
+    Unit u;
+    bool begins, whole;
+    int ui;
+    u.s = s;
+    u.len = kv_len(p.kv, s, p.whole);
+    if (p.whole) {
+      ui = (int)(x - (int64_t)s * p.U);
+      u.t0 = 0;
+      u.t1 = max(1, (u.len + Core::TK - 1) / Core::TK);
+      begins = whole = true;
+      ++x;
+    } else {
+      const int nt = pre[s + 1] - pre[s];
+      const int64_t rel = x - (int64_t)pre[s] * p.U;
+      ui = (int)(rel / nt);
+      u.t0 = (int)(rel - (int64_t)ui * nt);
+      u.t1 = (int)min((int64_t)nt, u.t0 + (end - x));
+      begins = u.t0 == 0;
+      whole = begins && u.t1 == nt;
+      x += u.t1 - u.t0;
+      if (ui == p.U - 1 && u.t1 == nt) ++s;
+    }
+    u.hk = ui / p.hb;
+    const int in_group = (ui - u.hk * p.hb) * Core::HT;
+    u.h0 = u.hk * p.G + in_group;
+    u.nh = min(Core::HT, p.G - in_group);
+
+    Core::run(p, u, ring, sq, s_m[warp], s_l[warp], warp, lane);
+    __syncthreads();
+    // join the warps; a finished unit writes O, a cut one its part
+    const int half = p.d >> 1;
+    for (int i = threadIdx.x; i < u.nh * half; i += NTHR) {
+      const int h = i / half, c = 2 * (i - h * half);
+      float M = s_m[0][h];
+#pragma unroll
+      for (int w = 1; w < WARPS; ++w) M = fmaxf(M, s_m[w][h]);
+      const float mu = M == -INFINITY ? 0.0f : M;
+      float L = 0.0f, a = 0.0f, b = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = ex2(s_m[w][h] - mu);
+        const float* src = reinterpret_cast<const float*>(smem + w * RING) + h * Core::LDB + c;
+        L = fmaf(f, s_l[w][h], L);
+        a = fmaf(f, src[0], a);
+        b = fmaf(f, src[1], b);
+      }
+      if (whole) {
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        const int64_t at = ((int64_t)u.s * p.h_r + u.h0 + h) * p.d + c;
+        if (p.o_f32) *reinterpret_cast<float2*>(p.O + 4 * at) = make_float2(a * inv, b * inv);
+        else *reinterpret_cast<uint32_t*>(p.O + 2 * at) = pack_bf16(a * inv, b * inv);
+        if (c == 0) {
+          const float v = L == 0.0f ? -INFINITY : mu + log2f(L);
+          const int64_t r = (int64_t)u.s * p.h_r + u.h0 + h;
+          if (p.lse2) p.lse2[r] = v;
+          if (p.lse) p.lse[r] = v * LN2;
+        }
+      } else {
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (begins ? 1 : 0);
+        *reinterpret_cast<float2*>(p.part_O + (slot * Core::HT + h) * p.d + c) = make_float2(a, b);
+        if (c == 0) p.part_ml[slot * Core::HT + h] = make_float2(M, L);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// CTA = (key chunk, sequence, key head).  Chunk 0 joins the parts of the units that were cut; with
+// scores every chunk turns its keys' x_j into weights and adds them up over the group.
+__global__ void __launch_bounds__(JOIN_THR) k_decode_join(const __grid_constant__ DecodeParams p, int HT) {
+  __shared__ float s_lse2[256];
+  const int rows = p.kv.nseq * p.h_kv;
+  const int chunk = blockIdx.x / rows, sg = blockIdx.x - chunk * rows;
+  const int s = sg / p.h_kv, hk = sg - s * p.h_kv;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int len = kv_len(p.kv, s, false);
+  const int64_t j0 = (int64_t)chunk * JOIN_KEYS;
+  if (chunk > 0 && j0 >= len) return;
+  int64_t per = 0, a0 = 0;
+  int nt = 1;
+  if (!p.whole) {
+    const int64_t total = (int64_t)p.pre[p.kv.nseq] * p.U;
+    per = tiles_per_cta(total, p.grid);
+    nt = p.pre[s + 1] - p.pre[s];
+    a0 = (int64_t)p.pre[s] * p.U;
+  }
+  for (int b = 0; b < p.hb; ++b) {
+    const int h0 = b * HT, nh = min(HT, p.G - h0);
+    int64_t c0 = 0, c1 = 0;
+    if (!p.whole) {
+      const int64_t at = a0 + (int64_t)(hk * p.hb + b) * nt;
+      c0 = at / per;
+      c1 = (at + nt - 1) / per;
+    }
+    if (c0 == c1) {
+      for (int h = threadIdx.x; h < nh; h += JOIN_THR)
+        s_lse2[h0 + h] = p.lse2 ? p.lse2[(int64_t)s * p.h_r + hk * p.G + h0 + h] : 0.0f;
+      continue;
+    }
+    // every thread repeats the statistics of its head, in CTA order
+    const int n = chunk == 0 ? nh * p.d : nh;
+    for (int i = threadIdx.x; i < n; i += JOIN_THR) {
+      const int h = chunk == 0 ? i / p.d : i, c = chunk == 0 ? i - h * p.d : 0;
+      float M = -INFINITY;
+      for (int64_t k = c0; k <= c1; ++k) M = fmaxf(M, p.part_ml[(2 * k + (k == c0)) * HT + h].x);
+      const float mu = M == -INFINITY ? 0.0f : M;
+      float L = 0.0f, acc = 0.0f;
+      for (int64_t k = c0; k <= c1; ++k) {
+        const int64_t slot = (2 * k + (k == c0)) * HT + h;
+        const float2 ml = p.part_ml[slot];
+        const float f = ex2(ml.x - mu);
+        L = fmaf(f, ml.y, L);
+        if (chunk == 0) acc = fmaf(f, p.part_O[slot * p.d + c], acc);
+      }
+      const float v = L == 0.0f ? -INFINITY : mu + log2f(L);
+      if (c == 0) s_lse2[h0 + h] = v;
+      if (chunk == 0) {
+        const int64_t r = (int64_t)s * p.h_r + hk * p.G + h0 + h;
+        acc = L == 0.0f ? 0.0f : acc * (1.0f / L);
+        if (p.o_f32) reinterpret_cast<float*>(p.O)[r * p.d + c] = acc;
+        else reinterpret_cast<__nv_bfloat16*>(p.O)[r * p.d + c] = __float2bfloat16_rn(acc);
+        if (c == 0 && p.lse) p.lse[r] = v * LN2;
+      }
+    }
+  }
+  if (!p.score_out) return;
+  __syncthreads();
+  const int64_t row = (int64_t)s * p.h_kv + hk;
+  const float* S = p.S + row * p.kv.max_len * p.GP;
+  const float* in = p.score_in ? p.score_in + row * p.score_stride : nullptr;
+  float* out = p.score_out + row * p.score_stride;
+  const int64_t j1 = min((int64_t)len, j0 + JOIN_KEYS);
+  for (int64_t j = j0 + threadIdx.x; j < j1; j += JOIN_THR) {
+    const float2* x = reinterpret_cast<const float2*>(S + j * p.GP);
+    float sum = 0.0f;
+    for (int h = 0; h < p.G; h += 2) {
+      const float2 v = x[h >> 1];
+      const float la = s_lse2[h];
+      sum += la == -INFINITY ? 0.0f : ex2(v.x - la);
+      if (h + 1 < p.G) {
+        const float lb = s_lse2[h + 1];
+        sum += lb == -INFINITY ? 0.0f : ex2(v.y - lb);
+      }
+    }
+    out[j] = (in ? in[j] : 0.0f) + sum;
+  }
+}
+
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// query heads per unit and keys per tile of the kernel that serves a descriptor
+int head_tile(const mf_paged_decode_desc& d) {
+  return d.kv.dtype == MF_BF16 && d.h_r / d.kv.h_kv > 8 ? 16 : 8;
+}
+
+// One CTA per unit, without a second launch, for lengths up to this many keys: splitting them
+// would leave a warp one or two tiles.
+constexpr int WHOLE_KEYS = 256;
+
+}  // namespace
+
+size_t paged_decode_ws(const mf_paged_decode_desc& d, PagedDecodeWs* ws, void* base) {
+  const int HT = head_tile(d), G = d.h_r / d.kv.h_kv, GP = (G + 1) & ~1;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* q = base ? static_cast<char*>(base) + at : nullptr;
+    at += up256(bytes);
+    return q;
+  };
+  char* pre = take(4 * ((size_t)d.kv.nseq + 1));
+  char* lse2 = take(4 * (size_t)d.kv.nseq * d.h_r);
+  char* po = take(sizeof(float) * 2 * MAX_GRID * (size_t)HT * d.kv.d);
+  char* ml = take(sizeof(float2) * 2 * MAX_GRID * (size_t)HT);
+  char* S = d.score_out ? take(4 * (size_t)d.kv.nseq * d.kv.h_kv * d.kv.max_len * GP) : nullptr;
+  if (ws) {
+    ws->pre = reinterpret_cast<int32_t*>(pre);
+    ws->lse2 = reinterpret_cast<float*>(lse2);
+    ws->part_O = reinterpret_cast<float*>(po);
+    ws->part_ml = reinterpret_cast<float2*>(ml);
+    ws->S = reinterpret_cast<float*>(S);
+  }
+  return at;
+}
+
+cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecodeWs& ws, uint32_t* status,
+                                cudaStream_t st) {
+  DecodeParams p{};
+  p.kv = kv_view(d.kv, status);
+  const int e = d.kv.dtype == MF_F32 ? 4 : 2;
+  p.Q = static_cast<const char*>(d.Q);
+  p.h_r = d.h_r;
+  p.h_kv = d.kv.h_kv;
+  p.d = d.kv.d;
+  p.G = d.h_r / d.kv.h_kv;
+  p.GP = (p.G + 1) & ~1;
+  const int HT = head_tile(d);
+  p.hb = (p.G + HT - 1) / HT;
+  p.U = p.h_kv * p.hb;
+  p.q_bytes = (d.q_stride ? d.q_stride : (int64_t)d.h_r * p.d) * e;
+  const double scale = d.scale > 0.0f ? (double)d.scale : 1.0 / std::sqrt((double)p.d);
+  p.c2 = (float)(scale * 1.4426950408889634074);
+  p.O = static_cast<char*>(d.O);
+  p.o_f32 = d.kv.dtype == MF_F32 || (d.flags & MF_DECODE_O_F32);
+  p.lse = d.lse;
+  p.S = d.score_out ? ws.S : nullptr;
+  p.score_in = d.score_in;
+  p.score_out = d.score_out;
+  p.score_stride = d.score_stride;
+  p.pre = ws.pre;
+  p.lse2 = ws.lse2;
+  p.part_O = ws.part_O;
+  p.part_ml = ws.part_ml;
+  p.whole = d.kv.max_len <= WHOLE_KEYS;
+
+  int dev = 0, sms = 0;
+  cudaError_t e0 = cudaGetDevice(&dev);
+  if (e0 == cudaSuccess) e0 = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e0 != cudaSuccess) return e0;
+
+  cudaError_t err = cudaSuccess;
+  auto launch = [&](auto core) {
+    using Core = decltype(core);
+    const size_t smem = (size_t)WARPS * Core::STAGES * Core::TILE + 4 * (size_t)Core::Q_FLOATS +
+                        (p.whole ? 0 : 4 * ((size_t)p.kv.nseq + 1));
+    auto kern = k_decode<Core>;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return;
+    p.grid = p.whole ? p.kv.nseq * p.U : std::min(MAX_GRID, sms * Core::CTAS);
+    kern<<<p.grid, NTHR, smem, st>>>(p);
+    err = cudaGetLastError();
+  };
+  const int D = p.d <= 64 ? 64 : p.d <= 128 ? 128 : p.d <= 192 ? 192 : 256;
+  if (d.kv.dtype == MF_F32) {
+    if (D == 64) launch(CoreF32<64>{});
+    else if (D == 128) launch(CoreF32<128>{});
+    else if (D == 192) launch(CoreF32<192>{});
+    else launch(CoreF32<256>{});
+  } else if (HT == 8) {
+    if (D == 64) launch(CoreBf16<64, 1>{});
+    else if (D == 128) launch(CoreBf16<128, 1>{});
+    else if (D == 192) launch(CoreBf16<192, 1>{});
+    else launch(CoreBf16<256, 1>{});
+  } else {
+    if (D == 64) launch(CoreBf16<64, 2>{});
+    else if (D == 128) launch(CoreBf16<128, 2>{});
+    else if (D == 192) launch(CoreBf16<192, 2>{});
+    else launch(CoreBf16<256, 2>{});
+  }
+  if (err != cudaSuccess || (p.whole && !p.score_out)) return err;
+
+  cudaLaunchConfig_t cfg{};
+  const int chunks = p.score_out ? (p.kv.max_len + JOIN_KEYS - 1) / JOIN_KEYS : 1;
+  cfg.gridDim = dim3((unsigned)std::max(1, chunks) * (unsigned)(p.kv.nseq * p.h_kv));
+  cfg.blockDim = dim3(JOIN_THR);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_decode_join, p, HT);
+}
+
+}  // namespace mfi

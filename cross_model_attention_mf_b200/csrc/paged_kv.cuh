@@ -1,0 +1,64 @@
+// The receiver's paged key-value cache as the kernels see it.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mf_internal.cuh"
+
+namespace mfi {
+
+struct KvView {
+  char* K;
+  char* V;
+  int64_t page_bytes;  // between pages
+  int32_t slot_bytes;  // h_kv * d * element: one slot's rows of every key head
+  int32_t row_bytes;   // d * element: one key head's row
+  int n_pages, page_size, max_pages, nseq, max_len;
+  const int32_t* table;
+  const int32_t* lens;
+  uint32_t* status;
+};
+
+inline KvView kv_view(const mf_paged_kv& k, uint32_t* status) {
+  const int e = k.dtype == MF_F32 ? 4 : 2;
+  KvView v;
+  v.K = static_cast<char*>(k.K);
+  v.V = static_cast<char*>(k.V);
+  v.row_bytes = k.d * e;
+  v.slot_bytes = k.h_kv * v.row_bytes;
+  v.page_bytes = k.page_stride ? k.page_stride * e : (int64_t)k.page_size * v.slot_bytes;
+  v.n_pages = k.n_pages;
+  v.page_size = k.page_size;
+  v.max_pages = k.max_pages;
+  v.nseq = k.nseq;
+  v.max_len = k.max_len;
+  v.table = k.block_table;
+  v.lens = k.seq_lens;
+  v.status = status;
+  return v;
+}
+
+// sequence length, within [0, max_len] and the table's slots; `report` sets the status bit for
+// one that is not
+__device__ __forceinline__ int kv_len(const KvView& v, int s, bool report) {
+  const int len = v.lens[s];
+  const int64_t room = (int64_t)v.max_pages * v.page_size;
+  const int top = room < v.max_len ? (int)room : v.max_len;
+  if (len >= 0 && len <= top) return len;
+  if (report) atomicOr(v.status, ST_INDEX);
+  return len < 0 ? 0 : top;
+}
+
+// byte offset (from K or V) of a slot's first head row, -1 for a page id out of range
+__device__ __forceinline__ int64_t kv_slot(const KvView& v, int s, int slot) {
+  const int pg = slot / v.page_size;
+  const int page = v.table[(int64_t)s * v.max_pages + pg];
+  if (page < 0 || page >= v.n_pages) {
+    atomicOr(v.status, ST_PAGE);
+    return -1;
+  }
+  return (int64_t)page * v.page_bytes + (int64_t)(slot - pg * v.page_size) * v.slot_bytes;
+}
+
+}  // namespace mfi

@@ -385,6 +385,175 @@ mf_status mf_cache_get(mf_block_cache* cache, int32_t layer, const uint64_t* has
 mf_status mf_cache_stats(mf_block_cache* cache, int64_t* out6);
 
 /* ------------------------------------------------------------------------------
+ * The receiver's paged key-value cache.  A receiver that took its prefill attention from a
+ * sender's maps decodes on its own keys and values.  Four calls carry its cache:
+ *   mf_kv_append       new tokens' keys and values into the pages;
+ *   mf_map_key_scores  the attention weight every key gathered during the prefill, from the
+ *                      compressed maps and the receiver's head map;
+ *   mf_paged_decode    attention of one new token per sequence, the gathered weights carried on;
+ *   mf_kv_evict        the cache cut back to a budget of slots by gathered weight.
+ * (The MapFlow pages name PagedAttention for the receiver's cache and say nothing of what
+ * follows the prefill; these calls are a property of this library.)
+ *
+ * Layout: K and V are [n_pages][page_size][h_kv][d] each (the paged V of mf_map_retrieve), pages
+ * page_stride elements apart, K and V in one dtype.  Slot j of sequence s is row j % page_size of
+ * page block_table[s * max_pages + j / page_size]; the sequence holds slots 0 .. seq_lens[s] - 1.
+ * Two sequences may list the same page for mf_paged_decode (a shared prefix); a page that
+ * mf_kv_append or mf_kv_evict writes must be listed once.
+ * A length below 0, above max_len or above max_pages * page_size is taken as the nearest bound
+ * and sets status bit 1; a page id outside [0, n_pages) sets status bit 16, its rows read as
+ * zeros and are not written.  Table entries past a sequence's last slot are not read.
+ *
+ * Scores and positions belong to (sequence, key head, slot): float32 score [nseq][h_kv][stride]
+ * and int32 pos [nseq][h_kv][stride], stride >= max_len.  pos holds the token position of each
+ * slot, which the slot number no longer tells once an eviction has moved rows.
+ *
+ * Requirements of all calls: d a multiple of 8, 8..256; K and V 16-byte aligned; page_stride a
+ * multiple of 16 bytes; 1 <= nseq <= 4096; 1 <= h_kv <= 64; nseq * max_len below 2^31.
+ * ------------------------------------------------------------------------------ */
+typedef struct {
+  void* K;                         /* device */
+  void* V;                         /* device */
+  mf_dtype dtype;                  /* K and V */
+  int64_t page_stride;             /* elements between pages; 0 = page_size * h_kv * d */
+  int32_t n_pages, page_size, max_pages;
+  int32_t h_kv, d;
+  const int32_t* block_table;      /* device [nseq][max_pages] */
+  const int32_t* seq_lens;         /* device [nseq] */
+  int32_t nseq;
+  int32_t max_len;                 /* host bound: every seq_lens[s] <= max_len */
+} mf_paged_kv;
+
+/* Attention of one new token per sequence over its cache.  For query head r of sequence s, key
+ * head g = r / (h_r / h_kv), slots j < seq_lens[s] (the new token's own slot among them):
+ *   x_j = scale * q_r . K[j][g],  lse = ln sum_j exp(x_j),  O_r = sum_j exp(x_j - lse) V[j][g].
+ * A sequence of length 0 gets O = 0 and lse = -inf, and so does a row whose every x_j is -inf;
+ * a NaN or +inf among the x_j makes the row NaN.
+ * Q: [nseq] rows of [h_r][d], q_stride elements apart (0 = h_r * d; a slice of a fused projection
+ * needs no copy).  O: [nseq][h_r][d] in the cache's dtype, or float32 with MF_DECODE_O_F32.  lse
+ * (optional): float [nseq][h_r].
+ * With score_out, the normalised weights are added up: score_out[s][g][j] = score_in[s][g][j] +
+ * sum over the heads r of group g of exp(x_j - lse), j < seq_lens[s]; later slots are left as
+ * they were.  score_in may be score_out itself; NULL stands for zeros.
+ * Arithmetic: bf16 keys and values run on tensor cores with float32 accumulation, the weights
+ * taking part as a bf16 pair (hi + lo, ~16 bits); float32 caches run in float32 throughout.
+ * Softmax statistics are float32.  The keys are split over the GPU by a rule on nseq, h_kv, the
+ * lengths and the number of SMs, and the parts are joined in a fixed order: repeated calls give
+ * the same bits.
+ * Requirements: h_r a multiple of h_kv, h_r <= 256; Q and O 16-byte aligned, q_stride a multiple
+ * of 16 bytes; scale finite and >= 0 (0 means 1 / sqrt(d)). */
+#define MF_DECODE_O_F32 1            /* flags: O is float32 */
+typedef struct {
+  mf_paged_kv kv;
+  const void* Q;                   /* device, dtype of the cache */
+  int64_t q_stride;
+  int32_t h_r;
+  float scale;
+  void* O;                         /* device out */
+  float* lse;                      /* device out, optional (NULL) */
+  const float* score_in;           /* device, optional (NULL) */
+  float* score_out;                /* device out, optional (NULL) */
+  int64_t score_stride;
+  int32_t flags;
+} mf_paged_decode_desc;
+
+/* Scratch bytes of mf_paged_decode (depends on nseq, max_len, h_kv, h_r, d and on whether
+ * score_out is set; with it, nseq * max_len * h_r * 4 bytes hold the scores x_j). */
+mf_status mf_paged_decode_workspace_size(const mf_paged_decode_desc* desc, size_t* bytes);
+
+/* Enqueue.  workspace: device, 256-byte aligned, not used by any other call until this one
+ * completes (two captured graphs that may run at the same time need one each). */
+mf_status mf_paged_decode(const mf_paged_decode_desc* desc, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* New tokens into the cache.  kv.seq_lens counts the new tokens already: sequence s's n =
+ * cu_seqlens_new[s+1] - cu_seqlens_new[s] new tokens (rows cu_seqlens_new[s] .. of K_new and
+ * V_new, each [h_kv][d], new_stride elements apart) take slots seq_lens[s] - n .. seq_lens[s] - 1.
+ * With score set those slots' scores become 0; with pos set their positions become
+ * n_seen[s] - n .. n_seen[s] - 1, n_seen[s] being the tokens of the sequence so far, the new ones
+ * among them (NULL: seq_lens, right until the first eviction).  Everything else is left as it
+ * was.  n < 0, n > max_new, n > seq_lens[s] or rows past total_new set status bit 1, and that
+ * sequence is skipped.
+ * Requirements: K_new and V_new 16-byte aligned, new_stride a multiple of 16 bytes (0 = h_kv * d). */
+typedef struct {
+  mf_paged_kv kv;
+  const void* K_new;               /* device, dtype of the cache */
+  const void* V_new;               /* device */
+  int64_t new_stride;
+  int64_t total_new;               /* rows of K_new and V_new */
+  const int32_t* cu_seqlens_new;   /* device [nseq + 1] */
+  int32_t max_new;                 /* host bound: every n <= max_new */
+  const int32_t* n_seen;           /* device [nseq], optional (NULL) */
+  float* score;                    /* device, optional (NULL) */
+  int32_t* pos;                    /* device, optional (NULL) */
+  int64_t score_stride;            /* of score and pos */
+} mf_kv_append_desc;
+
+mf_status mf_kv_append(const mf_kv_append_desc* desc, void* stream);
+
+/* Eviction by gathered weight.  For every (sequence s, key head g) with more than `budget` slots,
+ * `budget` of them are kept: first the protected ones, pos < sink or pos >= n_seen[s] - window
+ * (n_seen NULL: seq_lens), then by score, highest first, ties to the lowest slot (NaN counts as
+ * below -inf; -0 and 0 are equal).  The rest are dropped: kept rows whose slot is >= budget move,
+ * in slot order, into the dropped slots below budget, in slot order, so only they are copied.
+ * K and V change in place; score_out and pos_out [nseq][h_kv][stride] follow the rows, and get 0
+ * and -1 in slots [new length, old length); slots past the old length are left as they were.
+ * seq_lens_out[s] = min(seq_lens[s], budget).  score_out may be score_in, pos_out may be pos_in
+ * and seq_lens_out may be kv.seq_lens (partial overlaps are not allowed).
+ * Pages past the new length hold no live row afterwards and can be reused.
+ * Requirements: budget >= 1, sink >= 0, window >= 0, sink + window <= budget. */
+typedef struct {
+  mf_paged_kv kv;
+  const float* score_in;           /* device */
+  const int32_t* pos_in;           /* device */
+  float* score_out;                /* device out */
+  int32_t* pos_out;                /* device out */
+  int64_t score_stride;            /* of the four arrays */
+  const int32_t* n_seen;           /* device [nseq], optional (NULL) */
+  int32_t budget, sink, window;
+  int32_t* seq_lens_out;           /* device out [nseq] */
+} mf_kv_evict_desc;
+
+/* Scratch bytes of mf_kv_evict (depends on nseq, h_kv, max_len and budget). */
+mf_status mf_kv_evict_workspace_size(const mf_kv_evict_desc* desc, size_t* bytes);
+
+/* Enqueue.  workspace as for mf_paged_decode. */
+mf_status mf_kv_evict(const mf_kv_evict_desc* desc, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* Gathered weights at the end of a prefill that reused maps.  For receiver layer W [h_r][h_s] (one
+ * layer of mf_map_retrieve's W) and the sender layer's BSR, with P_r = sum_s W[r][s] A_s over the
+ * kept blocks:
+ *   score[s][g][j] = sum over heads r of group g, queries j <= i < L_s of P_r[i][j],  j < L_s.
+ * Sequence s has L_s = cu_seqlens[s+1] - cu_seqlens[s] tokens and the BSR rows qblock_base[s] ..
+ * + ceil(L_s / B) - 1.  Entries with j > i or i, j >= L_s are never used; slots j >= L_s are left
+ * as they were.  Column sums and head mix in float32, query blocks added in float64 in ascending
+ * order: repeated calls give the same bits.  A BSR row, column or length out of range sets status
+ * bit 1 and its blocks are skipped.
+ * Requirements: B in {32, 64, 128}; 1 <= h_s <= 256; h_r a multiple of h_kv, h_kv <= 64; values
+ * 16-byte aligned; at most 4096 query blocks per sequence; nseq <= 4096; n_rows < 2^24. */
+typedef struct {
+  mf_bsr bsr;
+  int64_t n_rows;                  /* rows of the BSR: row_ptr has n_rows + 1 entries */
+  mf_dtype map_dtype;
+  int32_t h_s, B;
+  const float* W;                  /* device [h_r][h_s] */
+  int32_t h_r, h_kv;
+  const int32_t* cu_seqlens;       /* device [nseq + 1] */
+  const int32_t* qblock_base;      /* device [nseq] */
+  int32_t nseq, max_seqlen;        /* host bound: every L_s <= max_seqlen */
+  float* score;                    /* device out [nseq][h_kv][score_stride] */
+  int64_t score_stride;            /* >= max_seqlen */
+} mf_key_scores_desc;
+
+/* Scratch bytes of mf_map_key_scores (capacity_blocks * h_kv * B * 4, and a part for each SM). */
+mf_status mf_map_key_scores_workspace_size(const mf_key_scores_desc* desc, size_t* bytes);
+
+/* Enqueue.  workspace as for mf_paged_decode. */
+mf_status mf_map_key_scores(const mf_key_scores_desc* desc, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* ------------------------------------------------------------------------------
  * Bounded waits (a property of this library; the MapFlow pages have no counterpart).
  * Every pipeline wait inside the tensor-core kernels (mf_map_retrieve and
  * mf_map_retrieve_multi on the tcgen05 path, mf_compress_qk, mf_calib_gram on the tcgen05
@@ -415,7 +584,8 @@ const char* mf_version(void);
 
 /* sizeof of this header's structs as the library was compiled, for bindings that
  * mirror them: which = 0 mf_compress_desc, 1 mf_bsr, 2 mf_retrieve_desc,
- * 3 mf_calib_desc, 4 mf_compress_qk_desc.
+ * 3 mf_calib_desc, 4 mf_compress_qk_desc, 5 mf_paged_decode_desc, 6 mf_kv_append_desc,
+ * 8 mf_kv_evict_desc, 9 mf_key_scores_desc.
  * Returns 0 for any other value. */
 size_t mf_abi_struct_size(int which);
 
