@@ -601,50 +601,92 @@ def choose_sender_layer(residuals_per_candidate: Sequence[torch.Tensor]) -> int:
 
 # ----------------------------------------------------------------------------- paged cache
 
-def _need(t, what, dtype, shape=None, device=None, contiguous=True):
-    """Refuse a tensor the kernels could not read as described."""
+def _at(t, what, dtype, shape, index, dense=True):
+    """Address of a tensor that is as the call needs it; any other is refused.  A decode step makes
+    these checks for some ten tensors, so the accepted case takes five calls and no more."""
+    try:
+        if t.dtype is dtype and t.get_device() == index >= 0 and t.shape == shape and \
+                (not dense or t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise ValueError(_fault(t, what, dtype, shape, index))
+
+
+def _fault(t, what, dtype, shape, index):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
+        return f"{what} must be a CUDA tensor"
     if t.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the call's other tensors on {device}")
-    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple('*' if n is None else n for n in shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+        return f"{what} must be {dtype}, not {t.dtype}"
+    if t.get_device() != index:
+        return f"{what} is on {t.device}, the call's other tensors on cuda:{index}"
+    if t.shape != shape:
+        return f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}"
+    return f"{what} must be contiguous"
 
 
-def _row_stride(t, what):
-    """Elements between the rows (dim 0) of t, whose other dims must be dense; 0 for one row."""
+def _sizes(t, what, dims):
+    """Shape of a tensor argument with `dims` dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {dims} dimensions")
+    return t.shape
+
+
+def _row_stride(a, b, what):
+    """Elements between the rows (dim 0) of a and b, which must agree; their other dims must be
+    dense.  0 for dense rows."""
+    if a.is_contiguous() and (b is None or b.is_contiguous()):
+        return 0
+    strides, shape = a.stride(), a.shape
+    if b is not None and b.stride() != strides and shape[0] > 1:
+        raise ValueError(f"{what} must have the same strides")
     step = 1
-    for k in range(t.dim() - 1, 0, -1):
-        if t.shape[k] != 1 and t.stride(k) != step:
+    for n, have in zip(shape[:0:-1], strides[:0:-1]):
+        if have != step and n != 1:
             raise ValueError(f"{what}: the dims after the first must be dense")
-        step *= t.shape[k]
-    return t.stride(0) if t.shape[0] > 1 and t.numel() else 0
+        step *= n
+    return strides[0] if shape[0] > 1 and step else 0
 
 
-def _scratch(need, workspace, device, stream):
-    """The caller's workspace, or one allocated here and kept from reuse until `stream` is done."""
-    if workspace is not None:
-        if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
-        return workspace
-    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if stream is not None:
-        workspace.record_stream(stream)
-    return workspace
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() without the Stream object
 
 
-def _enqueue(name, d, workspace, device, stream):
-    """Workspace and launch of one call on its tensors' device, on `stream` or the current one."""
-    fn = getattr(_lib, name)
-    with torch.cuda.device(device):
+def _on(index, stream):
+    return _raw_stream(index) if stream is None else stream.cuda_stream
+
+
+def _i32(n, what):
+    n = int(n)
+    if not -1 << 31 <= n < 1 << 31:  # ctypes would cut it off
+        raise ValueError(f"{what} = {n} does not fit 32 bits")
+    return n
+
+
+def _new(make, shape, dtype, index, stream):
+    """make (torch.empty or zeros) on the stream that will use the tensor: memory from another
+    stream's pool may still be in use there."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=index)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=index)
+
+
+def _enqueue(name, d, workspace, index, stream):
+    """Workspace and launch of one call on device `index`, on `stream` or the current one."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _enqueue(name, d, workspace, index, stream)
+    if workspace is None:
         need = ctypes.c_size_t(0)
-        _check(getattr(_lib, name + "_workspace_size")(ctypes.byref(d), ctypes.byref(need)))
-        ws = _scratch(max(need.value, 1), workspace, device, stream)
-        _check(fn(ctypes.byref(d), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+        _check(getattr(_lib, name + "_workspace_size")(d, need))
+        workspace = _new(torch.empty, max(need.value, 1), torch.uint8, index, stream)
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    rc = getattr(_lib, name)(d, workspace.data_ptr(), workspace.nbytes, _on(index, stream))
+    if rc:
+        _check(rc)
 
 
 @dataclass
@@ -669,25 +711,21 @@ class PagedKV:
         return self.K.device
 
     def desc(self) -> PagedKVDesc:
-        _dt(self.K)
-        _need(self.K, "K", self.K.dtype, (None,) * 4, contiguous=False)
-        _need(self.V, "V", self.K.dtype, tuple(self.K.shape), self.device, contiguous=False)
-        _need(self.block_table, "block_table", torch.int32, (None, None), self.device)
-        _need(self.seq_lens, "seq_lens", torch.int32, (self.nseq,), self.device)
-        stride = _row_stride(self.K, "K")
-        if _row_stride(self.V, "V") != stride:
-            raise ValueError("K and V must have the same page stride")
-        n_pages, page_size, h_kv, d = self.K.shape
-        return PagedKVDesc(_ptr(self.K), _ptr(self.V), _dt(self.K), stride, n_pages, page_size,
-                           self.block_table.shape[1], h_kv, d, _ptr(self.block_table),
-                           _ptr(self.seq_lens), self.nseq, int(self.max_len))
+        return self._plan()[0]
 
-
-def _score_pair(kv, a, b, dtype, what):
-    """Both arrays of a per-slot quantity: [nseq, h_kv, stride] with one stride."""
-    for t, w in ((a, what), (b, what + "_out")):
-        if t is not None:
-            _need(t, w, dtype, (kv.nseq, kv.h_kv, None if a is None else a.shape[2]), kv.device)
+    def _plan(self):
+        """Descriptor, device index, dtype, nseq, h_kv and d."""
+        K, V, table = self.K, self.V, self.block_table
+        code, index, shape = _dt(K), K.get_device(), _sizes(K, "K", 4)
+        n_pages, page_size, h_kv, d = shape
+        if n_pages >> 31 or page_size >> 31:
+            raise ValueError("n_pages and page_size must be below 2^31")
+        nseq, max_pages = wide = _sizes(table, "block_table", 2)
+        k, v = _at(K, "K", K.dtype, shape, index, False), _at(V, "V", K.dtype, shape, index, False)
+        return PagedKVDesc(k, v, code, _row_stride(K, V, "pages of K and V"), n_pages, page_size, max_pages,
+                           h_kv, d, _at(table, "block_table", torch.int32, wide, index),
+                           _at(self.seq_lens, "seq_lens", torch.int32, (nseq,), index), nseq,
+                           _i32(self.max_len, "max_len")), index, K.dtype, nseq, h_kv, d
 
 
 def mf_paged_decode_workspace_size(kv: PagedKV, h_r: int, scores: bool = False) -> int:
@@ -707,28 +745,31 @@ def mf_paged_decode(kv: PagedKV, Q: torch.Tensor, O: Optional[torch.Tensor] = No
                     o_f32: bool = False, workspace: Optional[torch.Tensor] = None,
                     stream=None) -> torch.Tensor:
     """Enqueue attention of one new token per sequence, Q [nseq, h_r, d] (rows may be strided),
-    over the cache; returns O [nseq, h_r, d] (allocated when None; float32 with o_f32).  scale 0
+    over the cache; returns O [nseq, h_r, d] (allocated on the call's stream when None; float32
+    with o_f32).  scale 0
     means 1 / sqrt(d).  lse: float32 [nseq, h_r] out.  score float32 [nseq, h_kv, stride]: the
     call's weights are added to it, into score_out when given, else in place; score_out alone
     receives the weights."""
-    kd = kv.desc()
-    dev = kv.device
-    _need(Q, "Q", kv.K.dtype, (kv.nseq, None, kv.K.shape[3]), dev, contiguous=False)
-    h_r = Q.shape[1]
+    kd, index, dtype, nseq, h_kv, d = kv._plan()
+    h_r = _sizes(Q, "Q", 3)[1]
+    shape = (nseq, h_r, d)
+    q = _at(Q, "Q", dtype, shape, index, False)
+    o_type = torch.float32 if o_f32 else dtype
     if O is None:
-        O = torch.empty((kv.nseq, h_r, Q.shape[2]), dtype=torch.float32 if o_f32 else Q.dtype, device=dev)
-        if stream is not None:
-            O.record_stream(stream)
-    _need(O, "O", torch.float32 if o_f32 else Q.dtype, (kv.nseq, h_r, Q.shape[2]), dev)
-    if lse is not None:
-        _need(lse, "lse", torch.float32, (kv.nseq, h_r), dev)
-    _score_pair(kv, score, score_out, torch.float32, "score")
-    if score_out is None:
-        score_out = score
-    d = PagedDecodeDesc(kd, _ptr(Q), _row_stride(Q, "Q"), h_r, float(scale), _ptr(O), _ptr(lse),
-                        _ptr(score), _ptr(score_out), 0 if score_out is None else score_out.shape[2],
-                        MF_DECODE_O_F32 if o_f32 else 0)
-    _enqueue("mf_paged_decode", d, workspace, dev, stream)
+        O = _new(torch.empty, shape, o_type, index, stream)
+    o = _at(O, "O", o_type, shape, index)
+    l = None if lse is None else _at(lse, "lse", torch.float32, (nseq, h_r), index)
+    s_in = s_out = None
+    wide = 0
+    if score is not None or score_out is not None:
+        wide = _sizes(score_out if score is None else score, "score", 3)[2]
+        if score is not None:
+            s_in = s_out = _at(score, "score", torch.float32, (nseq, h_kv, wide), index)
+        if score_out is not None:
+            s_out = _at(score_out, "score_out", torch.float32, (nseq, h_kv, wide), index)
+    _enqueue("mf_paged_decode",
+             PagedDecodeDesc(kd, q, _row_stride(Q, None, "Q"), h_r, float(scale), o, l, s_in, s_out, wide,
+                             MF_DECODE_O_F32 if o_f32 else 0), workspace, index, stream)
     return O
 
 
@@ -739,26 +780,27 @@ def mf_kv_append(kv: PagedKV, K_new: torch.Tensor, V_new: torch.Tensor, cu_seqle
     """Enqueue the copy of new tokens' K_new, V_new [T, h_kv, d] (rows may be strided) into the
     cache, whose seq_lens already count them; their scores become 0 and their positions
     n_seen - n .. n_seen - 1 where score / pos [nseq, h_kv, stride] are given."""
-    kd = kv.desc()
-    dev = kv.device
-    shape = (None, kv.h_kv, kv.K.shape[3])
-    _need(K_new, "K_new", kv.K.dtype, shape, dev, contiguous=False)
-    _need(V_new, "V_new", kv.K.dtype, tuple(K_new.shape), dev, contiguous=False)
-    _need(cu_seqlens_new, "cu_seqlens_new", torch.int32, (kv.nseq + 1,), dev)
-    stride = _row_stride(K_new, "K_new")
-    if _row_stride(V_new, "V_new") != stride:
-        raise ValueError("K_new and V_new must have the same row stride")
-    if n_seen is not None:
-        _need(n_seen, "n_seen", torch.int32, (kv.nseq,), dev)
-    wide = None
-    for t, what, dt in ((score, "score", torch.float32), (pos, "pos", torch.int32)):
-        if t is not None:
-            _need(t, what, dt, (kv.nseq, kv.h_kv, wide), dev)
-            wide = t.shape[2]
-    d = KvAppendDesc(kd, _ptr(K_new), _ptr(V_new), stride, K_new.shape[0], _ptr(cu_seqlens_new),
-                     int(max_new), _ptr(n_seen), _ptr(score), _ptr(pos), wide or 0)
-    with torch.cuda.device(dev):
-        _check(_lib.mf_kv_append(ctypes.byref(d), _stream(stream)))
+    kd, index, dtype, nseq, h_kv, d = kv._plan()
+    T = _sizes(K_new, "K_new", 3)[0]
+    shape = (T, h_kv, d)
+    k, v = _at(K_new, "K_new", dtype, shape, index, False), _at(V_new, "V_new", dtype, shape, index, False)
+    cu = _at(cu_seqlens_new, "cu_seqlens_new", torch.int32, (nseq + 1,), index)
+    seen = None if n_seen is None else _at(n_seen, "n_seen", torch.int32, (nseq,), index)
+    wide, s, p = 0, None, None
+    if score is not None or pos is not None:
+        wide = _sizes(pos if score is None else score, "score", 3)[2]
+        if score is not None:
+            s = _at(score, "score", torch.float32, (nseq, h_kv, wide), index)
+        if pos is not None:
+            p = _at(pos, "pos", torch.int32, (nseq, h_kv, wide), index)
+    desc = KvAppendDesc(kd, k, v, _row_stride(K_new, V_new, "rows of K_new and V_new"), T, cu,
+                        _i32(max_new, "max_new"), seen, s, p, wide)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _check(_lib.mf_kv_append(desc, _on(index, stream)))
+    rc = _lib.mf_kv_append(desc, _on(index, stream))
+    if rc:
+        _check(rc)
 
 
 def mf_kv_evict_workspace_size(kv: PagedKV, budget: int) -> int:
@@ -780,19 +822,20 @@ def mf_kv_evict(kv: PagedKV, score: torch.Tensor, pos: torch.Tensor, budget: int
     rows past the budget move into the dropped slots.  score float32 and pos int32
     [nseq, h_kv, stride] follow, in place unless score_out / pos_out are given.  Returns the new
     lengths: seq_lens_out, or kv.seq_lens updated in place."""
-    kd = kv.desc()
-    dev = kv.device
-    _score_pair(kv, score, score_out, torch.float32, "score")
-    _need(pos, "pos", torch.int32, tuple(score.shape), dev)
-    _score_pair(kv, pos, pos_out, torch.int32, "pos")
-    if n_seen is not None:
-        _need(n_seen, "n_seen", torch.int32, (kv.nseq,), dev)
+    kd, index, _, nseq, h_kv, _ = kv._plan()
+    wide = _sizes(score, "score", 3)[2]
+    shape = (nseq, h_kv, wide)
+    s_out = s_in = _at(score, "score", torch.float32, shape, index)
+    p_out = p_in = _at(pos, "pos", torch.int32, shape, index)
+    if score_out is not None:
+        s_out = _at(score_out, "score_out", torch.float32, shape, index)
+    if pos_out is not None:
+        p_out = _at(pos_out, "pos_out", torch.int32, shape, index)
+    seen = None if n_seen is None else _at(n_seen, "n_seen", torch.int32, (nseq,), index)
     out = kv.seq_lens if seq_lens_out is None else seq_lens_out
-    _need(out, "seq_lens_out", torch.int32, (kv.nseq,), dev)
-    d = KvEvictDesc(kd, _ptr(score), _ptr(pos), _ptr(score if score_out is None else score_out),
-                    _ptr(pos if pos_out is None else pos_out), score.shape[2], _ptr(n_seen),
-                    int(budget), int(sink), int(window), _ptr(out))
-    _enqueue("mf_kv_evict", d, workspace, dev, stream)
+    left = _at(out, "seq_lens_out", torch.int32, (nseq,), index)
+    _enqueue("mf_kv_evict", KvEvictDesc(kd, s_in, p_in, s_out, p_out, wide, seen, _i32(budget, "budget"),
+                                        _i32(sink, "sink"), _i32(window, "window"), left), workspace, index, stream)
     return out
 
 
@@ -812,27 +855,26 @@ def mf_map_key_scores(bsr: BSR, W: torch.Tensor, cu_seqlens: torch.Tensor, qbloc
                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Enqueue the weights that every key of every sequence gathered in a prefill over reused maps:
     one receiver layer's W float32 [h_r, h_s], one sender layer's BSR.  Returns score float32
-    [nseq, h_kv, stride >= max_seqlen] (allocated as zeros when None); slots past a sequence's
+    [nseq, h_kv, stride >= max_seqlen] (zeros allocated on the call's stream when None); slots past a sequence's
     length are left as they were."""
-    dev = bsr.values.device
-    _dt(bsr.values)
-    _need(bsr.values, "values", bsr.values.dtype, (None,) * 4, dev)
-    _need(bsr.row_ptr, "row_ptr", torch.int32, (None,), dev)
-    _need(bsr.col_idx, "col_idx", torch.int32, (None,), dev)
-    cap, h_s, B, B2 = bsr.values.shape
-    if B2 != B or bsr.col_idx.numel() < cap or bsr.row_ptr.numel() < 1:
+    h_kv, max_seqlen = _i32(h_kv, "h_kv"), _i32(max_seqlen, "max_seqlen")
+    values, row_ptr = bsr.values, bsr.row_ptr
+    code, index = _dt(values), values.get_device()
+    cap, h_s, B, B2 = shape = _sizes(values, "values", 4)
+    rows, h_r = _sizes(row_ptr, "row_ptr", 1), _sizes(W, "W", 2)[0]
+    kept = _sizes(bsr.col_idx, "col_idx", 1)
+    if B2 != B or kept[0] < cap or rows[0] < 1:
         raise ValueError("values must be [capacity, h_s, B, B], col_idx [capacity], row_ptr [rows + 1]")
-    _need(W, "W", torch.float32, (None, h_s), dev)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (None,), dev)
-    nseq = cu_seqlens.numel() - 1
-    _need(qblock_base, "qblock_base", torch.int32, (max(nseq, 0),), dev)
+    blocks = BsrDesc(_at(row_ptr, "row_ptr", torch.int32, rows, index),
+                     _at(bsr.col_idx, "col_idx", torch.int32, kept, index),
+                     _at(values, "values", values.dtype, shape, index), cap)
+    nseq = _sizes(cu_seqlens, "cu_seqlens", 1)[0] - 1
     if score is None:
-        score = torch.zeros((nseq, h_kv, max(int(max_seqlen), 1)), dtype=torch.float32, device=dev)
-        if stream is not None:
-            score.record_stream(stream)
-    _need(score, "score", torch.float32, (nseq, h_kv, None), dev)
-    d = KeyScoresDesc(bsr.desc(), bsr.row_ptr.numel() - 1, _dt(bsr.values), h_s, B, _ptr(W),
-                      W.shape[0], int(h_kv), _ptr(cu_seqlens), _ptr(qblock_base), nseq,
-                      int(max_seqlen), _ptr(score), score.shape[2])
-    _enqueue("mf_map_key_scores", d, workspace, dev, stream)
+        score = _new(torch.zeros, (nseq, h_kv, max(max_seqlen, 1)), torch.float32, index, stream)
+    wide = _sizes(score, "score", 3)[2]
+    d = KeyScoresDesc(blocks, rows[0] - 1, code, h_s, B, _at(W, "W", torch.float32, (h_r, h_s), index), h_r, h_kv,
+                      _at(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), index),
+                      _at(qblock_base, "qblock_base", torch.int32, (nseq,), index), nseq, max_seqlen,
+                      _at(score, "score", torch.float32, (nseq, h_kv, wide), index), wide)
+    _enqueue("mf_map_key_scores", d, workspace, index, stream)
     return score

@@ -24,9 +24,17 @@ mf_status fail(mf_status s, const std::string& msg) {
   return s;
 }
 
+constexpr int kMaxDevices = 64;
+
+// address of the current device's status word; looked up once per device
 uint32_t* status_ptr() {
-  void* p = nullptr;
+  static std::atomic<void*> known[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  void* p = dev < kMaxDevices ? known[dev].load(std::memory_order_acquire) : nullptr;
+  if (p) return static_cast<uint32_t*>(p);
   if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) return nullptr;
+  if (dev < kMaxDevices) known[dev].store(p, std::memory_order_release);
   return static_cast<uint32_t*>(p);
 }
 
@@ -97,7 +105,6 @@ mf_status check_retrieve(const mf_retrieve_desc* d) {
 // symbol, never a device address: the address is looked up per device below.
 static __device__ __align__(256) unsigned char g_static_ws[MF_STATIC_WORKSPACE_BYTES];
 
-constexpr int kMaxDevices = 64;
 std::mutex g_static_mu;
 void* g_static_ptr[kMaxDevices];  // device address of g_static_ws, per device (null: not yet)
 
