@@ -31,8 +31,10 @@ constexpr int WARPS = 4;
 constexpr int NTHR = 32 * WARPS;
 constexpr int MAX_GRID = 512;     // CTAs of the main kernel (two partial results each)
 constexpr int MIN_TILES = WARPS;  // tiles a CTA takes at least: one per warp
+constexpr int MAX_SEQS = 4096;    // as the entry point checks
 constexpr int JOIN_THR = 256;
-constexpr int JOIN_KEYS = 2048;   // keys per CTA of the join kernel
+constexpr int JOIN_KEYS = 2048;   // keys whose weights a CTA of the join kernel adds up
+constexpr int MAX_JOINERS = 2048; // CTAs of the join kernel that add up parts
 constexpr float LN2 = 0.693147180559945309f;
 
 struct DecodeParams {
@@ -599,85 +601,154 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
   }
 }
 
-// CTA = (key chunk, sequence, key head).  Chunk 0 joins the parts of the units that were cut; with
-// scores every chunk turns its keys' x_j into weights and adds them up over the group.
-__global__ void __launch_bounds__(JOIN_THR) k_decode_join(const __grid_constant__ DecodeParams p, int HT) {
-  __shared__ float s_lse2[256];
-  const int rows = p.kv.nseq * p.h_kv;
-  const int chunk = blockIdx.x / rows, sg = blockIdx.x - chunk * rows;
-  const int s = sg / p.h_kv, hk = sg - s * p.h_kv;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int len = kv_len(p.kv, s, false);
-  const int64_t j0 = (int64_t)chunk * JOIN_KEYS;
-  if (chunk > 0 && j0 >= len) return;
-  int64_t per = 0, a0 = 0;
-  int nt = 1;
-  if (!p.whole) {
-    const int64_t total = (int64_t)p.pre[p.kv.nseq] * p.U;
-    per = tiles_per_cta(total, p.grid);
-    nt = p.pre[s + 1] - p.pre[s];
-    a0 = (int64_t)p.pre[s] * p.U;
+// Parts of one unit: CTAs c0 .. c1 hold one each when c0 < c1; c0 == c1 when one CTA finished it.
+struct Parts {
+  int64_t c0;
+  int n;  // c1 - c0 + 1
+  __device__ int64_t slot(int k) const { return 2 * (c0 + k) + (k == 0); }
+};
+
+__device__ __forceinline__ Parts unit_parts(const DecodeParams& p, int s, int ui) {
+  if (p.whole) return {0, 1};
+  const int64_t total = (int64_t)p.pre[p.kv.nseq] * p.U;
+  const int64_t per = tiles_per_cta(total, p.grid);
+  const int nt = p.pre[s + 1] - p.pre[s];
+  const int64_t at = (int64_t)p.pre[s] * p.U + (int64_t)ui * nt;
+  const int64_t c0 = at / per;
+  return {c0, (int)((at + nt - 1) / per - c0) + 1};
+}
+
+// m (0 for an empty row) and l of head h over the parts: one warp, the same in every lane
+__device__ __forceinline__ float2 join_stats(const DecodeParams& p, const Parts& u, int HT, int h, int lane) {
+  float M = -INFINITY;
+  for (int k = lane; k < u.n; k += 32) M = fmaxf(M, p.part_ml[u.slot(k) * HT + h].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+  const float mu = M == -INFINITY ? 0.0f : M;
+  float L = 0.0f;
+  for (int k = lane; k < u.n; k += 32) {
+    const float2 ml = p.part_ml[u.slot(k) * HT + h];
+    L = fmaf(ex2(ml.x - mu), ml.y, L);
   }
-  for (int b = 0; b < p.hb; ++b) {
-    const int h0 = b * HT, nh = min(HT, p.G - h0);
-    int64_t c0 = 0, c1 = 0;
-    if (!p.whole) {
-      const int64_t at = a0 + (int64_t)(hk * p.hb + b) * nt;
-      c0 = at / per;
-      c1 = (at + nt - 1) / per;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(~0u, L, o);
+  return make_float2(mu, L);
+}
+
+// sum over the group's heads of 2^(x - lse2), V heads to a load
+template <int V>
+__device__ __forceinline__ float key_weight(const float* x, const float* lse2, int GP) {
+  float sum = 0.0f;
+  for (int h = 0; h < GP; h += V) {
+    float v[V];
+    if (V == 4) {
+      const float4 t = __ldcs(reinterpret_cast<const float4*>(x + h));
+      v[0] = t.x, v[1] = t.y, v[V - 2] = t.z, v[V - 1] = t.w;
+    } else {
+      const float2 t = __ldcs(reinterpret_cast<const float2*>(x + h));
+      v[0] = t.x, v[1] = t.y;
     }
-    if (c0 == c1) {
-      for (int h = threadIdx.x; h < nh; h += JOIN_THR)
-        s_lse2[h0 + h] = p.lse2 ? p.lse2[(int64_t)s * p.h_r + hk * p.G + h0 + h] : 0.0f;
-      continue;
-    }
-    // every thread repeats the statistics of its head, in CTA order
-    const int n = chunk == 0 ? nh * p.d : nh;
-    for (int i = threadIdx.x; i < n; i += JOIN_THR) {
-      const int h = chunk == 0 ? i / p.d : i, c = chunk == 0 ? i - h * p.d : 0;
-      float M = -INFINITY;
-      for (int64_t k = c0; k <= c1; ++k) M = fmaxf(M, p.part_ml[(2 * k + (k == c0)) * HT + h].x);
-      const float mu = M == -INFINITY ? 0.0f : M;
-      float L = 0.0f, acc = 0.0f;
-      for (int64_t k = c0; k <= c1; ++k) {
-        const int64_t slot = (2 * k + (k == c0)) * HT + h;
-        const float2 ml = p.part_ml[slot];
-        const float f = ex2(ml.x - mu);
-        L = fmaf(f, ml.y, L);
-        if (chunk == 0) acc = fmaf(f, p.part_O[slot * p.d + c], acc);
-      }
-      const float v = L == 0.0f ? -INFINITY : mu + log2f(L);
-      if (c == 0) s_lse2[h0 + h] = v;
-      if (chunk == 0) {
-        const int64_t r = (int64_t)s * p.h_r + hk * p.G + h0 + h;
-        acc = L == 0.0f ? 0.0f : acc * (1.0f / L);
-        if (p.o_f32) reinterpret_cast<float*>(p.O)[r * p.d + c] = acc;
-        else reinterpret_cast<__nv_bfloat16*>(p.O)[r * p.d + c] = __float2bfloat16_rn(acc);
-        if (c == 0 && p.lse) p.lse[r] = v * LN2;
-      }
-    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += lse2[h + i] == INFINITY ? 0.0f : ex2(v[i] - lse2[h + i]);
   }
-  if (!p.score_out) return;
-  __syncthreads();
-  const int64_t row = (int64_t)s * p.h_kv + hk;
+  return sum;
+}
+
+template <int V>
+__device__ __forceinline__ void add_weights(const DecodeParams& p, int64_t row, int j0, int j1, const float* lse2) {
   const float* S = p.S + row * p.kv.max_len * p.GP;
   const float* in = p.score_in ? p.score_in + row * p.score_stride : nullptr;
   float* out = p.score_out + row * p.score_stride;
-  const int64_t j1 = min((int64_t)len, j0 + JOIN_KEYS);
-  for (int64_t j = j0 + threadIdx.x; j < j1; j += JOIN_THR) {
-    const float2* x = reinterpret_cast<const float2*>(S + j * p.GP);
-    float sum = 0.0f;
-    for (int h = 0; h < p.G; h += 2) {
-      const float2 v = x[h >> 1];
-      const float la = s_lse2[h];
-      sum += la == -INFINITY ? 0.0f : ex2(v.x - la);
-      if (h + 1 < p.G) {
-        const float lb = s_lse2[h + 1];
-        sum += lb == -INFINITY ? 0.0f : ex2(v.y - lb);
-      }
-    }
-    out[j] = (in ? in[j] : 0.0f) + sum;
+  constexpr int UN = 4;
+  for (int j = j0 + threadIdx.x; j < j1; j += UN * JOIN_THR) {
+    float old[UN], w[UN];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) old[i] = in && j + i * JOIN_THR < j1 ? in[j + i * JOIN_THR] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < UN; ++i)
+      w[i] = j + i * JOIN_THR < j1 ? key_weight<V>(S + (int64_t)(j + i * JOIN_THR) * p.GP, lse2, p.GP) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < UN; ++i)
+      if (j + i * JOIN_THR < j1) out[j + i * JOIN_THR] = old[i] + w[i];
   }
+}
+
+// The first `joiners` CTAs add up the parts of the units that were cut, a query head at a time:
+// the threads take 16 bytes of the row each, the parts in slices that are added up in order.  The
+// others, one per (key chunk, sequence, key head), turn the x_j into weights and add them up over
+// the group.  Both find the row's lse from the parts' (m, l), lanes over parts.
+__global__ void __launch_bounds__(JOIN_THR) k_decode_join(const __grid_constant__ DecodeParams p, int HT, int joiners) {
+  __shared__ float s_lse2[256 + 4];
+  __shared__ float4 s_acc[JOIN_THR];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if ((int)blockIdx.x < joiners) {
+    const int nc = p.d >> 2, ns = JOIN_THR / nc;  // 16-byte columns, slices
+    const int c = tid % nc, sl = tid / nc;
+    for (int r0 = blockIdx.x; r0 < p.kv.nseq * p.h_r; r0 += joiners) {
+      const int s = r0 / p.h_r, r = r0 - s * p.h_r;
+      const int hk = r / p.G, b = (r - hk * p.G) / HT, h = r - hk * p.G - b * HT;
+      const Parts u = unit_parts(p, s, hk * p.hb + b);
+      if (u.n == 1) continue;
+      const float2 ml = join_stats(p, u, HT, h, lane);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (sl < ns)
+#pragma unroll 4
+        for (int k = sl; k < u.n; k += ns) {
+          const int64_t at = u.slot(k) * HT + h;
+          const float f = ex2(p.part_ml[at].x - ml.x);
+          const float4 v = reinterpret_cast<const float4*>(p.part_O + at * p.d)[c];
+          a.x = fmaf(f, v.x, a.x);
+          a.y = fmaf(f, v.y, a.y);
+          a.z = fmaf(f, v.z, a.z);
+          a.w = fmaf(f, v.w, a.w);
+        }
+      s_acc[tid] = a;
+      __syncthreads();
+      if (tid < nc) {
+        for (int k = 1; k < min(ns, u.n); ++k) {
+          const float4 v = s_acc[k * nc + tid];
+          a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+        }
+        const float inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
+        const int64_t at = (int64_t)r0 * p.d + 4 * tid;
+        if (p.o_f32) {
+          *reinterpret_cast<float4*>(p.O + 4 * at) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+        } else {
+          *reinterpret_cast<uint2*>(p.O + 2 * at) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+        }
+        if (tid == 0 && p.lse) p.lse[r0] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * LN2;
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  const int rows = p.kv.nseq * p.h_kv, job = blockIdx.x - joiners;
+  const int chunk = job / rows, sg = job - chunk * rows;
+  const int s = sg / p.h_kv, hk = sg - s * p.h_kv;
+  const int len = kv_len(p.kv, s, false);
+  const int64_t j0 = (int64_t)chunk * JOIN_KEYS;
+  if (j0 >= len) return;
+  // lse2 of the group's heads; +inf stands for an empty row and for the padding, whose weights are 0
+  for (int h = warp; h < p.GP; h += JOIN_THR / 32) {
+    float v = INFINITY;
+    if (h < p.G) {
+      const int b = h / HT;
+      const Parts u = unit_parts(p, s, hk * p.hb + b);
+      if (u.n == 1) {
+        v = p.lse2[(int64_t)s * p.h_r + hk * p.G + h];
+      } else {
+        const float2 ml = join_stats(p, u, HT, h - b * HT, lane);
+        v = ml.y == 0.0f ? -INFINITY : ml.x + log2f(ml.y);
+      }
+      if (v == -INFINITY) v = INFINITY;
+    }
+    if (lane == 0) s_lse2[h] = v;
+  }
+  __syncthreads();
+  const int j1 = (int)min((int64_t)len, j0 + JOIN_KEYS);
+  if (p.GP % 4 == 0) add_weights<4>(p, sg, (int)j0, j1, s_lse2);
+  else add_weights<2>(p, sg, (int)j0, j1, s_lse2);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -756,11 +827,11 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
     using Core = decltype(core);
     const size_t smem = (size_t)WARPS * Core::STAGES * Core::TILE + 4 * (size_t)Core::Q_FLOATS +
                         (p.whole ? 0 : 4 * ((size_t)p.kv.nseq + 1));
-    auto kern = k_decode<Core>;
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // room for the scan of the largest batch
+    err = allow_smem<&k_decode<Core>>(dev, WARPS * Core::STAGES * Core::TILE + 4 * Core::Q_FLOATS + 4 * (MAX_SEQS + 1));
     if (err != cudaSuccess) return;
     p.grid = p.whole ? p.kv.nseq * p.U : std::min(MAX_GRID, sms * Core::CTAS);
-    kern<<<p.grid, NTHR, smem, st>>>(p);
+    k_decode<Core><<<p.grid, NTHR, smem, st>>>(p);
     err = cudaGetLastError();
   };
   const int D = p.d <= 64 ? 64 : p.d <= 128 ? 128 : p.d <= 192 ? 192 : 256;
@@ -783,8 +854,10 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   if (err != cudaSuccess || (p.whole && !p.score_out)) return err;
 
   cudaLaunchConfig_t cfg{};
-  const int chunks = p.score_out ? (p.kv.max_len + JOIN_KEYS - 1) / JOIN_KEYS : 1;
-  cfg.gridDim = dim3((unsigned)std::max(1, chunks) * (unsigned)(p.kv.nseq * p.h_kv));
+  const int joiners = p.whole ? 0 : std::min(MAX_JOINERS, p.kv.nseq * p.h_r);
+  const int chunks = p.score_out ? (p.kv.max_len + JOIN_KEYS - 1) / JOIN_KEYS : 0;
+  cfg.gridDim = dim3((unsigned)joiners + (unsigned)chunks * (unsigned)(p.kv.nseq * p.h_kv));
+  if (cfg.gridDim.x == 0) return cudaSuccess;
   cfg.blockDim = dim3(JOIN_THR);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -792,7 +865,7 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_decode_join, p, HT);
+  return cudaLaunchKernelEx(&cfg, k_decode_join, p, HT, joiners);
 }
 
 }  // namespace mfi
