@@ -5,10 +5,13 @@
 // Eviction keeps `budget` of a (sequence, key head)'s slots.  With k_j the 32-bit key whose
 // unsigned order is the order of preference (protected slots above all, then the score),
 // the kept set is the `budget` largest keys, equal keys by slot.  k_evict_select finds the
-// smallest kept key by counting: three rounds over 11, 11 and 10 bits, each a histogram of the
-// slots that still share the prefix, walked from the top.  A cluster of CTAs shares one (sequence,
-// key head): the keys stay in its shared memory, the histograms are added over distributed shared
-// memory, so scores and positions are read once however long the cache.
+// smallest kept key by counting: up to three rounds over 11, 11 and 10 bits, each a histogram of
+// the slots that still share the prefix, walked from the top; a round whose bin is kept whole is
+// the last.  A cluster of CTAs shares one (sequence, key head): the keys stay in its shared
+// memory, the histograms are added over distributed shared memory, so scores and positions are
+// read once before the kept ones are copied.
+// With kb(j) kept slots before slot j, hole j is the (j - kb(j))-th and mover j the
+// (kb(j) - kb(new length))-th: one count over the cluster places both.
 // Attention does not depend on the order of the slots, so kept rows below the budget stay where
 // they are and only the kept rows above it move, into the dropped slots: every source lies at or
 // above the budget and every target below, so all moves are independent and k_evict_move makes
@@ -91,12 +94,12 @@ __global__ void __launch_bounds__(AP_THR) k_append(const __grid_constant__ Appen
 }
 
 // ------------------------------------------------------------------ eviction: selection
-constexpr int EV_THR = 512;
-constexpr int EV_WARPS = EV_THR / 32;
 constexpr int BINS = 2048;
-constexpr int EV_KEYS = 32768;    // keys a CTA keeps in shared memory; later ones are read again
 constexpr int EV_CLUSTER = 8;     // portable cluster size
+constexpr int EV_LOADS = 8;       // slots a thread loads at a time
 constexpr int EV_SLOTS = 4096;    // slots a CTA takes before the cluster grows
+constexpr int EV_THR = 256;       // threads of a CTA, or
+constexpr int EV_WIDE = 512;      // where a cluster of the smaller ones cannot hold the row
 
 struct EvictParams {
   KvView kv;
@@ -109,7 +112,6 @@ struct EvictParams {
   int budget, sink, window, h_kv;
   int32_t* lens_out;
   KvEvictWs ws;
-  int keys;           // capacity of the shared key array
 };
 
 // unsigned order = preference: NaN below -inf, then ascending scores, protected slots on top
@@ -120,198 +122,251 @@ __device__ __forceinline__ uint32_t evict_key(float score, int pos, int sink, in
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// exclusive scan of one count per thread over the CTA
-__device__ __forceinline__ uint32_t scan_excl(uint32_t a, uint32_t* s_w) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = a;
+__device__ __forceinline__ uint32_t scan_warp(uint32_t x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t u = __shfl_up_sync(~0u, x, o);
     if (lane >= o) x += u;
   }
-  if (lane == 31) s_w[warp] = x;
-  __syncthreads();
-  uint32_t r = x - a;
-#pragma unroll
-  for (int w = 0; w < EV_WARPS; ++w)
-    if (w < warp) r += s_w[w];
-  __syncthreads();
-  return r;
+  return x;
 }
 
-__global__ void __launch_bounds__(EV_THR) k_evict_select(const __grid_constant__ EvictParams p) {
+// A CTA's slots are one tile of at most 32 THR, whose keys stay in shared memory, or are read
+// again, tile by tile, in every pass.  A warp owns up to 32 groups of 32 neighbouring slots of a
+// tile; ballots mark a group's keys above the bar and at it, lane q keeps the marks of group q,
+// and one scan over the lanes counts them all (a population count per group and pass took four
+// times as long, and loops unrolled over the slots twice: the code no longer fits the
+// instruction cache).
+template <int THR>
+__global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_constant__ EvictParams p) {
+  constexpr int WARPS = THR / 32, TILE = THR * 32, OWN = BINS / THR;
+  static_assert(OWN % 4 == 0, "");
   extern __shared__ uint32_t s_key[];
-  __shared__ uint32_t s_hist[BINS];
-  __shared__ uint32_t s_a[EV_WARPS], s_b[EV_WARPS];
-  __shared__ uint32_t s_pick[2];    // bin of the smallest kept key, keys still to take from it
-  __shared__ uint32_t s_count[2];   // this CTA's counts, read by the cluster
+  __shared__ __align__(16) uint32_t s_hist[2][BINS];
+  __shared__ uint32_t s_scan[2][WARPS];
+  __shared__ uint32_t s_pick[2][3];           // bin of the smallest kept key, keys to take from it, keys in it
+  __shared__ uint2 s_cnt[WARPS];              // keys above and at the bar, per warp of the tile
+  __shared__ __align__(16) uint32_t s_tot[4]; // of the CTA: above, at the bar; and of those, below the new length
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int job = blockIdx.x / C;
   const int s = job / p.h_kv;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool first = job == s * p.h_kv && rank == 0 && tid == 0;
   // the move kernel may take its place; it waits for this grid before its first access
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int len = kv_len(p.kv, s, rank == 0 && tid == 0 && job == s * p.h_kv);
+  const int len = kv_len(p.kv, s, first);
+  const int64_t recent = (int64_t)(p.n_seen ? p.n_seen[s] : len) - p.window;
   const int left = min(len, p.budget);
   const int64_t row = (int64_t)job * p.stride;
   const float* sc = p.score_in + row;
   const int32_t* po = p.pos_in + row;
-  const bool cut = len > p.budget;
+  const bool copy_s = p.score_out != p.score_in, copy_p = p.pos_out != p.pos_in;
   // slots of this CTA
   const int per = (len + C - 1) / C;
   const int lo = min(len, rank * per), hi = min(len, lo + per);
-  const int64_t recent = (int64_t)(p.n_seen ? p.n_seen[s] : len) - p.window;
-  if (job == s * p.h_kv && rank == 0 && tid == 0) p.ws.len[s] = left;
-
-  if (!cut) {  // nothing goes: the rows stay, copies follow
+  if (first) p.ws.len[s] = left;
+  if (len <= p.budget) {  // nothing goes: the rows stay, copies follow
     if (rank == 0 && tid == 0) p.ws.count[job] = 0;
-    for (int j = lo + tid; j < hi; j += EV_THR) {
-      if (p.score_out != p.score_in) p.score_out[row + j] = sc[j];
-      if (p.pos_out != p.pos_in) p.pos_out[row + j] = po[j];
-    }
+    if (copy_s || copy_p)
+#pragma unroll 8
+      for (int j = lo + tid; j < hi; j += THR) {
+        if (copy_s) p.score_out[row + j] = sc[j];
+        if (copy_p) p.pos_out[row + j] = po[j];
+      }
     return;  // the whole cluster: len is the same for its CTAs
   }
-
-  auto key_of = [&](int j) -> uint32_t {
-    const int i = j - lo;
-    return i < p.keys ? s_key[i] : evict_key(sc[j], po[j], p.sink, recent);
+  auto sync = [&] {
+    if (C == 1) __syncthreads(); else cl.sync();
   };
+  auto load = [&](int t0, int n) {  // keys of the tile's n slots
+    for (int i0 = tid; i0 < n; i0 += EV_LOADS * THR) {
+      float a[EV_LOADS];
+      int b[EV_LOADS];
+#pragma unroll
+      for (int k = 0; k < EV_LOADS; ++k)
+        if (i0 + k * THR < n) {
+          a[k] = sc[t0 + i0 + k * THR];
+          b[k] = po[t0 + i0 + k * THR];
+        }
+#pragma unroll
+      for (int k = 0; k < EV_LOADS; ++k)
+        if (i0 + k * THR < n) s_key[i0 + k * THR] = evict_key(a[k], b[k], p.sink, recent);
+    }
+  };
+  const bool one = hi - lo <= TILE;
+  for (int i = tid; i < 2 * BINS / 4; i += THR) reinterpret_cast<uint4*>(s_hist)[i] = make_uint4(0, 0, 0, 0);
+  if (tid < 4) s_tot[tid] = 0;
+  if (one) load(lo, hi - lo);
+  __syncthreads();
+
   uint32_t prefix = 0, need = (uint32_t)p.budget;
+  int shift = 32;  // bits below the prefix
 #pragma unroll 1
   for (int round = 0; round < 3; ++round) {
-    const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
-    const uint32_t mask = round == 2 ? 1023u : 2047u;
-    const int top = round == 0 ? 32 : shift + (round == 1 ? 11 : 10);  // bits above are the prefix
-    for (int b = tid; b < BINS; b += EV_THR) s_hist[b] = 0;
-    __syncthreads();
-    for (int j = lo + tid; j < hi; j += EV_THR) {
-      uint32_t k;
-      if (round == 0) {
-        k = evict_key(sc[j], po[j], p.sink, recent);
-        if (j - lo < p.keys) s_key[j - lo] = k;
-      } else {
-        k = key_of(j);
+    const int top = shift, buf = round & 1;
+    shift = round == 0 ? 21 : round == 1 ? 10 : 0;
+    const uint32_t mask = (1u << (top - shift)) - 1u;
+    uint32_t* hist = s_hist[buf];
+    for (int t0 = lo; t0 < hi; t0 += TILE) {
+      const int n = min(TILE, hi - t0);
+      if (!one) load(t0, n);  // every thread counts the keys that it wrote itself
+#pragma unroll 4
+      for (int i = tid; i < n; i += THR) {
+        const uint32_t k = s_key[i];
+        if (round == 0 || k >> top == prefix) atomicAdd(&hist[(k >> shift) & mask], 1u);
       }
-      if (round == 0 || k >> top == prefix) atomicAdd(&s_hist[(k >> shift) & mask], 1u);
     }
-    cl.sync();
-    // every CTA adds up the cluster's histograms and walks them from the top: thread t owns bins
-    // 4 t .. 4 t + 3 counted from the highest
-    uint32_t c[4];
+    sync();
+    // every CTA adds up the cluster's histograms and walks them from the top: thread t owns OWN
+    // bins, thread 0 the highest
+    const int b0 = BINS - (tid + 1) * OWN;
+    uint32_t c[OWN];
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) c[i] = 0;
+#pragma unroll 4
+    for (int r = 0; r < C; ++r) {
+      const uint32_t* from = C == 1 ? hist : cl.map_shared_rank(hist, r);
+#pragma unroll
+      for (int i = 0; i < OWN; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(from + b0 + i);
+        c[i] += v.x, c[i + 1] += v.y, c[i + 2] += v.z, c[i + 3] += v.w;
+      }
+    }
     uint32_t sum = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = BINS - 1 - (4 * tid + i);
-      uint32_t v = 0;
-      for (int r = 0; r < C; ++r) v += *cl.map_shared_rank(&s_hist[b], r);
-      c[i] = v;
-      sum += v;
-    }
-    uint32_t above = scan_excl(sum, s_a);
+    for (int i = 0; i < OWN; ++i) sum += c[i];
+    const uint32_t incl = scan_warp(sum, lane);
+    if (lane == 31) s_scan[buf][warp] = incl;
+    if (round == 1)  // the first histogram has been read everywhere: it serves the third round
+      for (int i = tid; i < BINS / 4; i += THR) reinterpret_cast<uint4*>(s_hist[0])[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    uint32_t above = incl - sum;
+    for (int w = 0; w < warp; ++w) above += s_scan[buf][w];
+    if (above < need && need <= above + sum) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (above < need && need <= above + c[i]) {
-        s_pick[0] = (uint32_t)(BINS - 1 - (4 * tid + i));
-        s_pick[1] = need - above;
+      for (int i = OWN - 1; i >= 0; --i) {
+        if (above < need && need <= above + c[i]) {
+          s_pick[buf][0] = (uint32_t)(b0 + i);
+          s_pick[buf][1] = need - above;
+          s_pick[buf][2] = c[i];
+        }
+        above += c[i];
       }
-      above += c[i];
     }
-    cl.sync();  // the histograms have been read everywhere, and s_pick is written
-    prefix = round == 0 ? s_pick[0] : (prefix << (round == 1 ? 11 : 10)) | s_pick[0];
-    need = s_pick[1];
+    __syncthreads();
+    prefix = (prefix << (top - shift)) | s_pick[buf][0];
+    need = s_pick[buf][1];
+    if (s_pick[buf][2] == need) break;  // the same in the whole cluster
   }
-  const uint32_t bar = prefix;  // smallest kept key; `need` of the slots that equal it are kept
+  // kept: keys whose upper bits are above the prefix, and the first `need` of those that equal it
 
-  // slots in order, a contiguous run per warp, 32 at a time: the equal keys before a slot decide
-  // its fate
-  const int lane = tid & 31, warp = tid >> 5;
   const uint32_t below = (1u << lane) - 1u;
-  const int run = ((hi - lo + EV_THR - 1) / EV_THR) * 32;
-  const int w0 = min(hi, lo + warp * run), w1 = min(hi, w0 + run);
-  uint32_t eq = 0;
-  for (int j = w0; j < w1; j += 32) eq += __popc(__ballot_sync(~0u, j + lane < w1 && key_of(j + lane) == bar));
-  if (lane == 0) s_a[warp] = eq;
-  __syncthreads();
-  uint32_t eq_before = 0;
-  if (tid == 0) s_count[0] = 0;
-  for (int w = 0; w < EV_WARPS; ++w) {
-    if (w < warp) eq_before += s_a[w];
-    if (tid == 0) s_count[0] += s_a[w];
-  }
-  cl.sync();
-  for (int r = 0; r < rank; ++r) eq_before += *cl.map_shared_rank(&s_count[0], r);
-  // holes: dropped slots below the new length; movers: kept slots at or above it
-  uint32_t e = eq_before, holes = 0, movers = 0;
-  for (int j0 = w0; j0 < w1; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t k = j < w1 ? key_of(j) : 0u;
-    const uint32_t eqm = __ballot_sync(~0u, j < w1 && k == bar);
-    const bool kept = k > bar || (k == bar && e + __popc(eqm & below) < need);
-    e += __popc(eqm);
-    holes += __popc(__ballot_sync(~0u, j < w1 && !kept && j < left));
-    movers += __popc(__ballot_sync(~0u, j < w1 && kept && j >= left));
-  }
-  if (lane == 0) {
-    s_a[warp] = holes;
-    s_b[warp] = movers;
-  }
-  cl.sync();  // the equal keys' counts have been read everywhere
-  uint32_t h = 0, mv = 0, th = 0, tm = 0;
-  for (int w = 0; w < EV_WARPS; ++w) {
-    if (w < warp) {
-      h += s_a[w];
-      mv += s_b[w];
+  uint32_t mg = 0, me = 0;  // marks of this lane's group: above the bar, at it
+  int g0 = 0, groups = 0;   // first slot of the warp within the tile, its groups
+  auto marks = [&](int n) {
+    groups = (n + THR - 1) / THR;
+    g0 = warp * groups * 32;
+    mg = me = 0;
+#pragma unroll 4
+    for (int q = 0; q < groups; ++q) {
+      const int i = g0 + 32 * q + lane;
+      const uint32_t u = i < n ? s_key[i] >> shift : 0u;
+      const uint32_t g = __ballot_sync(~0u, i < n && u > prefix), e = __ballot_sync(~0u, i < n && u == prefix);
+      if (lane == q) mg = g, me = e;
     }
-    th += s_a[w];
-    tm += s_b[w];
-  }
-  if (tid == 0) {
-    s_count[0] = th;
-    s_count[1] = tm;
-  }
-  cl.sync();
-  uint32_t total = 0;
-  for (int r = 0; r < C; ++r) {
-    const uint32_t m = *cl.map_shared_rank(&s_count[1], r);
-    if (r < rank) {
-      h += *cl.map_shared_rank(&s_count[0], r);
-      mv += m;
+  };
+  for (int t0 = lo; t0 < hi; t0 += TILE) {
+    const int n = min(TILE, hi - t0);
+    if (!one) {
+      __syncthreads();
+      load(t0, n);
+      __syncthreads();
     }
-    total += m;
+    marks(n);
+    // slots of the lane's group that lie below the new length
+    const int in = min(32, max(0, left - (t0 + g0 + 32 * lane)));
+    const uint32_t lm = in == 32 ? ~0u : (1u << in) - 1u;
+    const uint32_t gt = __reduce_add_sync(~0u, __popc(mg)), eq = __reduce_add_sync(~0u, __popc(me));
+    const uint32_t gt_l = __reduce_add_sync(~0u, __popc(mg & lm)), eq_l = __reduce_add_sync(~0u, __popc(me & lm));
+    if (lane == 0) {
+      s_cnt[warp] = make_uint2(gt, eq);
+      atomicAdd(&s_tot[0], gt);
+      atomicAdd(&s_tot[1], eq);
+      atomicAdd(&s_tot[2], gt_l);
+      atomicAdd(&s_tot[3], eq_l);
+    }
   }
-  if (rank == 0 && tid == 0) p.ws.count[job] = (int32_t)total;
+  sync();
+  uint32_t gt_before, eq_before, kept_l;  // before this CTA; kept below the new length
+  {
+    uint4 t = make_uint4(0, 0, 0, 0);
+    if (lane < C) t = *reinterpret_cast<const uint4*>(C == 1 ? s_tot : cl.map_shared_rank(s_tot, lane));
+    gt_before = __reduce_add_sync(~0u, lane < rank ? t.x : 0u);
+    eq_before = __reduce_add_sync(~0u, lane < rank ? t.y : 0u);
+    kept_l = __reduce_add_sync(~0u, t.z) + min(need, __reduce_add_sync(~0u, t.w));
+  }
+  if (C > 1) cl.sync();  // no CTA leaves while another still reads its totals
+  if (rank == 0 && tid == 0) p.ws.count[job] = p.budget - (int32_t)kept_l;
   int32_t* dst = p.ws.dst + (int64_t)job * p.ws.moves;
   int32_t* src = p.ws.src + (int64_t)job * p.ws.moves;
-  e = eq_before;
-  for (int j0 = w0; j0 < w1; j0 += 32) {
-    const int j = j0 + lane;
-    const bool in = j < w1;
-    const uint32_t k = in ? key_of(j) : 0u;
-    const uint32_t eqm = __ballot_sync(~0u, in && k == bar);
-    const bool kept = k > bar || (k == bar && e + __popc(eqm & below) < need);
-    e += __popc(eqm);
-    const uint32_t hm = __ballot_sync(~0u, in && !kept && j < left);
-    const uint32_t mm = __ballot_sync(~0u, in && kept && j >= left);
-    if (in) {
-      if (j < left) {
-        if (!kept) {
-          dst[h + __popc(hm & below)] = j;
-        } else {
-          if (p.score_out != p.score_in) p.score_out[row + j] = sc[j];
-          if (p.pos_out != p.pos_in) p.pos_out[row + j] = po[j];
+  for (int t0 = lo; t0 < hi; t0 += TILE) {
+    const int n = min(TILE, hi - t0);
+    if (!one) {
+      __syncthreads();
+      load(t0, n);
+      __syncthreads();
+      marks(n);
+      const uint32_t gt = __reduce_add_sync(~0u, __popc(mg)), eq = __reduce_add_sync(~0u, __popc(me));
+      if (lane == 0) s_cnt[warp] = make_uint2(gt, eq);
+      __syncthreads();
+    }
+    uint32_t g = gt_before, e = eq_before;
+    for (int w = 0; w < WARPS; ++w) {
+      const uint2 c = s_cnt[w];
+      if (w < warp) g += c.x, e += c.y;
+      gt_before += c.x, eq_before += c.y;
+    }
+    // keys above and at the bar before the lane's group
+    g += scan_warp(__popc(mg), lane) - __popc(mg);
+    e += scan_warp(__popc(me), lane) - __popc(me);
+    for (int q0 = 0; q0 < groups; q0 += 4) {
+      float a[4];
+      int b[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = g0 + 32 * (q0 + k) + lane, j = t0 + i;
+        if (q0 + k < groups && i < n && j < left) {
+          if (copy_s) a[k] = sc[j];
+          if (copy_p) b[k] = po[j];
         }
-      } else if (kept) {
-        src[mv + __popc(mm & below)] = j;  // its score and position move with the row
-      } else {
-        p.score_out[row + j] = 0.0f;
-        p.pos_out[row + j] = -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int q = q0 + k;  // below 32: groups <= 32
+        const uint32_t gm = __shfl_sync(~0u, mg, q), em = __shfl_sync(~0u, me, q);
+        const uint32_t eb = __shfl_sync(~0u, e, q) + __popc(em & below);                      // equal keys before the slot
+        const uint32_t kb = __shfl_sync(~0u, g, q) + __popc(gm & below) + min(need, eb);      // kept slots before it
+        const bool kept = (gm >> lane & 1u) || ((em >> lane & 1u) && eb < need);
+        const int i = g0 + 32 * q + lane, j = t0 + i;
+        if (q < groups && i < n) {
+          if (j < left) {
+            if (!kept) {
+              dst[j - kb] = j;
+            } else {
+              if (copy_s) p.score_out[row + j] = a[k];
+              if (copy_p) p.pos_out[row + j] = b[k];
+            }
+          } else if (kept) {
+            src[kb - kept_l] = j;  // its score and position move with the row
+          } else {
+            p.score_out[row + j] = 0.0f;
+            p.pos_out[row + j] = -1;
+          }
+        }
       }
     }
-    h += __popc(hm);
-    mv += __popc(mm);
   }
-  cl.sync();  // no CTA leaves while another still reads its counts
 }
 
 // ------------------------------------------------------------------ eviction: moves
@@ -431,26 +486,30 @@ cudaError_t launch_kv_evict(const mf_kv_evict_desc& d, const KvEvictWs& ws, uint
   p.lens_out = d.seq_lens_out;
   p.ws = ws;
   const int jobs = d.kv.nseq * d.kv.h_kv;
+  // CTAs of 256 threads share a row, EV_SLOTS of its slots each, as long as a cluster of them
+  // holds it; a longer row takes CTAs of 512
+  const bool wide = d.kv.max_len > (int64_t)EV_CLUSTER * 32 * EV_THR;
+  const int64_t most = 32 * (wide ? EV_WIDE : EV_THR);
   int C = 1;
   while (C < EV_CLUSTER && (int64_t)C * EV_SLOTS < d.kv.max_len) C *= 2;
-  p.keys = (int)std::min<int64_t>(EV_KEYS, ((int64_t)d.kv.max_len + C - 1) / C);
-  const size_t smem = 4 * (size_t)p.keys;
-  cudaError_t e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       4 * EV_KEYS);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = wide ? allow_smem<&k_evict_select<EV_WIDE>>(dev, 4 * 32 * EV_WIDE)
+                                 : allow_smem<&k_evict_select<EV_THR>>(dev, 4 * 32 * EV_THR);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3((unsigned)((int64_t)jobs * C));
-  cfg.blockDim = dim3(EV_THR);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(wide ? EV_WIDE : EV_THR);
+  cfg.dynamicSmemBytes = 4 * (size_t)std::min<int64_t>(most, ((int64_t)d.kv.max_len + C - 1) / C);
   cfg.stream = st;
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)C;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k_evict_select, p);
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  e = wide ? cudaLaunchKernelEx(&cfg, k_evict_select<EV_WIDE>, p) : cudaLaunchKernelEx(&cfg, k_evict_select<EV_THR>, p);
   if (e != cudaSuccess) return e;
 
   const int chunks = (int)std::max<int64_t>(1, (ws.moves + MV_ROWS - 1) / MV_ROWS);
