@@ -12,6 +12,8 @@
 // read once before the kept ones are copied.
 // With kb(j) kept slots before slot j, hole j is the (j - kb(j))-th and mover j the
 // (kb(j) - kb(new length))-th: one count over the cluster places both.
+// What bounds the selection is the number of instructions per slot, next to the latency of a
+// round (histogram, barrier, walk), not the bytes.
 // Attention does not depend on the order of the slots, so kept rows below the budget stay where
 // they are and only the kept rows above it move, into the dropped slots: every source lies at or
 // above the budget and every target below, so all moves are independent and k_evict_move makes
@@ -115,11 +117,12 @@ struct EvictParams {
 };
 
 // unsigned order = preference: NaN below -inf, then ascending scores, protected slots on top
-__device__ __forceinline__ uint32_t evict_key(float score, int pos, int sink, int64_t recent) {
-  if (pos < sink || pos >= recent) return 0xFFFFFFFFu;
-  if (score != score) return 0u;
-  const uint32_t b = __float_as_uint(score == 0.0f ? 0.0f : score);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+__device__ __forceinline__ uint32_t evict_key(float score, int pos, int sink, int recent) {
+  const uint32_t b = __float_as_uint(score + 0.0f);  // -0 becomes 0
+  uint32_t k = b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+  if (score != score) k = 0u;
+  if (pos < sink || pos >= recent) k = 0xFFFFFFFFu;
+  return k;
 }
 
 __device__ __forceinline__ uint32_t scan_warp(uint32_t x, int lane) {
@@ -131,37 +134,53 @@ __device__ __forceinline__ uint32_t scan_warp(uint32_t x, int lane) {
   return x;
 }
 
+// the lowest n set bits of m
+__device__ __forceinline__ uint32_t lowest_bits(uint32_t m, uint32_t n) {
+  if (n >= __popc(m)) return m;
+  uint32_t r = 0;
+  for (; n && m; --n) {
+    r |= m & (0u - m);
+    m &= m - 1;
+  }
+  return r;
+}
+
 // A CTA's slots are one tile of at most 32 THR, whose keys stay in shared memory, or are read
 // again, tile by tile, in every pass.  A warp owns up to 32 groups of 32 neighbouring slots of a
-// tile; ballots mark a group's keys above the bar and at it, lane q keeps the marks of group q,
-// and one scan over the lanes counts them all (a population count per group and pass took four
-// times as long, and loops unrolled over the slots twice: the code no longer fits the
-// instruction cache).
-template <int THR>
+// tile; ballots mark a group's keys above the bar and at it, and lane q keeps the marks of group
+// q: what is kept, a hole or a mover is then found for 1024 slots at once.
+// SOLO: one CTA has the row to itself.
+template <int THR, bool SOLO>
 __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_constant__ EvictParams p) {
   constexpr int WARPS = THR / 32, TILE = THR * 32, OWN = BINS / THR;
   static_assert(OWN % 4 == 0, "");
-  extern __shared__ uint32_t s_key[];
+  extern __shared__ __align__(16) uint32_t s_key[];
   __shared__ __align__(16) uint32_t s_hist[2][BINS];
   __shared__ uint32_t s_scan[2][WARPS];
   __shared__ uint32_t s_pick[2][3];           // bin of the smallest kept key, keys to take from it, keys in it
   __shared__ uint2 s_cnt[WARPS];              // keys above and at the bar, per warp of the tile
   __shared__ __align__(16) uint32_t s_tot[4]; // of the CTA: above, at the bar; and of those, below the new length
   cg::cluster_group cl = cg::this_cluster();
-  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int C = SOLO ? 1 : (int)cl.num_blocks(), rank = SOLO ? 0 : (int)cl.block_rank();
   const int job = blockIdx.x / C;
   const int s = job / p.h_kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool first = job == s * p.h_kv && rank == 0 && tid == 0;
   // the move kernel may take its place; it waits for this grid before its first access
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int seen = p.n_seen ? p.n_seen[s] : 0;
   const int len = kv_len(p.kv, s, first);
-  const int64_t recent = (int64_t)(p.n_seen ? p.n_seen[s] : len) - p.window;
+  for (int i = tid; i < 2 * BINS / 4; i += THR) reinterpret_cast<uint4*>(s_hist)[i] = make_uint4(0, 0, 0, 0);
+  if (tid < 4) s_tot[tid] = 0;
+  // a bound below -2^31 protects every slot, as -2^31 does
+  const int recent = (int)max((int64_t)INT32_MIN, (int64_t)(p.n_seen ? seen : len) - p.window);
   const int left = min(len, p.budget);
   const int64_t row = (int64_t)job * p.stride;
   const float* sc = p.score_in + row;
   const int32_t* po = p.pos_in + row;
-  const bool copy_s = p.score_out != p.score_in, copy_p = p.pos_out != p.pos_in;
+  float* so = p.score_out + row;
+  int32_t* qo = p.pos_out + row;
+  const bool copy_s = so != sc, copy_p = qo != po;
   // slots of this CTA
   const int per = (len + C - 1) / C;
   const int lo = min(len, rank * per), hi = min(len, lo + per);
@@ -171,34 +190,57 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
     if (copy_s || copy_p)
 #pragma unroll 8
       for (int j = lo + tid; j < hi; j += THR) {
-        if (copy_s) p.score_out[row + j] = sc[j];
-        if (copy_p) p.pos_out[row + j] = po[j];
+        if (copy_s) so[j] = sc[j];
+        if (copy_p) qo[j] = po[j];
       }
     return;  // the whole cluster: len is the same for its CTAs
   }
   auto sync = [&] {
-    if (C == 1) __syncthreads(); else cl.sync();
+    if (SOLO) __syncthreads(); else cl.sync();
   };
-  auto load = [&](int t0, int n) {  // keys of the tile's n slots
+  const bool one = hi - lo <= TILE;
+  // Keys of the tile's n slots.  The first pass counts their upper bits, and writes outputs that
+  // are not the inputs: slots below the new length as they are (the movers overwrite the holes
+  // later), cleared ones above it.
+  auto load = [&](int t0, int n, bool begin) {
     for (int i0 = tid; i0 < n; i0 += EV_LOADS * THR) {
+      const int rem = n - i0, keep = left - t0 - i0;
+      const float* ps = sc + t0 + i0;
+      const int32_t* pp = po + t0 + i0;
       float a[EV_LOADS];
       int b[EV_LOADS];
 #pragma unroll
       for (int k = 0; k < EV_LOADS; ++k)
-        if (i0 + k * THR < n) {
-          a[k] = sc[t0 + i0 + k * THR];
-          b[k] = po[t0 + i0 + k * THR];
+        if (k * THR < rem) {
+          a[k] = ps[k * THR];
+          b[k] = pp[k * THR];
         }
+      uint32_t* pk = s_key + i0;
 #pragma unroll
       for (int k = 0; k < EV_LOADS; ++k)
-        if (i0 + k * THR < n) s_key[i0 + k * THR] = evict_key(a[k], b[k], p.sink, recent);
+        if (k * THR < rem) {
+          const uint32_t key = evict_key(a[k], b[k], p.sink, recent);
+          pk[k * THR] = key;
+          if (begin) atomicAdd(&s_hist[0][key >> 21], 1u);
+        }
+      if (begin && copy_s) {
+        float* out = so + t0 + i0;
+#pragma unroll
+        for (int k = 0; k < EV_LOADS; ++k)
+          if (k * THR < rem) out[k * THR] = k * THR < keep ? a[k] : 0.0f;
+      }
+      if (begin && copy_p) {
+        int32_t* out = qo + t0 + i0;
+#pragma unroll
+        for (int k = 0; k < EV_LOADS; ++k)
+          if (k * THR < rem) out[k * THR] = k * THR < keep ? b[k] : -1;
+      }
     }
+    // the last vector of keys is read whole: zeros count below every budget
+    if (tid < (-n & 3)) s_key[n + tid] = 0;
   };
-  const bool one = hi - lo <= TILE;
-  for (int i = tid; i < 2 * BINS / 4; i += THR) reinterpret_cast<uint4*>(s_hist)[i] = make_uint4(0, 0, 0, 0);
-  if (tid < 4) s_tot[tid] = 0;
-  if (one) load(lo, hi - lo);
   __syncthreads();
+  for (int t0 = lo; t0 < hi; t0 += TILE) load(t0, min(TILE, hi - t0), true);
 
   uint32_t prefix = 0, need = (uint32_t)p.budget;
   int shift = 32;  // bits below the prefix
@@ -206,15 +248,24 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
   for (int round = 0; round < 3; ++round) {
     const int top = shift, buf = round & 1;
     shift = round == 0 ? 21 : round == 1 ? 10 : 0;
-    const uint32_t mask = (1u << (top - shift)) - 1u;
     uint32_t* hist = s_hist[buf];
-    for (int t0 = lo; t0 < hi; t0 += TILE) {
-      const int n = min(TILE, hi - t0);
-      if (!one) load(t0, n);  // every thread counts the keys that it wrote itself
-#pragma unroll 4
-      for (int i = tid; i < n; i += THR) {
-        const uint32_t k = s_key[i];
-        if (round == 0 || k >> top == prefix) atomicAdd(&hist[(k >> shift) & mask], 1u);
+    if (round > 0) {
+      const uint32_t mask = (1u << (top - shift)) - 1u;
+      for (int t0 = lo; t0 < hi; t0 += TILE) {
+        const int n = min(TILE, hi - t0);
+        if (!one) {
+          __syncthreads();
+          load(t0, n, false);
+          __syncthreads();
+        }
+#pragma unroll 2
+        for (int i = tid; i < (n + 3) >> 2; i += THR) {
+          const uint4 v = reinterpret_cast<const uint4*>(s_key)[i];
+          if (v.x >> top == prefix) atomicAdd(&hist[(v.x >> shift) & mask], 1u);
+          if (v.y >> top == prefix) atomicAdd(&hist[(v.y >> shift) & mask], 1u);
+          if (v.z >> top == prefix) atomicAdd(&hist[(v.z >> shift) & mask], 1u);
+          if (v.w >> top == prefix) atomicAdd(&hist[(v.w >> shift) & mask], 1u);
+        }
       }
     }
     sync();
@@ -226,7 +277,7 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
     for (int i = 0; i < OWN; ++i) c[i] = 0;
 #pragma unroll 4
     for (int r = 0; r < C; ++r) {
-      const uint32_t* from = C == 1 ? hist : cl.map_shared_rank(hist, r);
+      const uint32_t* from = SOLO ? hist : cl.map_shared_rank(hist, r);
 #pragma unroll
       for (int i = 0; i < OWN; i += 4) {
         const uint4 v = *reinterpret_cast<const uint4*>(from + b0 + i);
@@ -241,8 +292,7 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
     if (round == 1)  // the first histogram has been read everywhere: it serves the third round
       for (int i = tid; i < BINS / 4; i += THR) reinterpret_cast<uint4*>(s_hist[0])[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    uint32_t above = incl - sum;
-    for (int w = 0; w < warp; ++w) above += s_scan[buf][w];
+    uint32_t above = incl - sum + __reduce_add_sync(~0u, lane < warp ? s_scan[buf][lane] : 0u);
     if (above < need && need <= above + sum) {
 #pragma unroll
       for (int i = OWN - 1; i >= 0; --i) {
@@ -261,32 +311,34 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
   }
   // kept: keys whose upper bits are above the prefix, and the first `need` of those that equal it
 
-  const uint32_t below = (1u << lane) - 1u;
-  uint32_t mg = 0, me = 0;  // marks of this lane's group: above the bar, at it
-  int g0 = 0, groups = 0;   // first slot of the warp within the tile, its groups
-  auto marks = [&](int n) {
-    groups = (n + THR - 1) / THR;
+  uint32_t mg = 0, me = 0;      // marks of this lane's group: above the bar, at it
+  uint32_t lm = 0, vm = 0;      // its slots below the new length, its slots
+  int g0 = 0;                   // the warp's first slot
+  auto marks = [&](int t0, int n) {
+    const int groups = (n + THR - 1) / THR;
     g0 = warp * groups * 32;
+    const uint32_t* pk = s_key + g0 + lane;
+    const int rem = n - g0 - lane;
     mg = me = 0;
 #pragma unroll 4
     for (int q = 0; q < groups; ++q) {
-      const int i = g0 + 32 * q + lane;
-      const uint32_t u = i < n ? s_key[i] >> shift : 0u;
-      const uint32_t g = __ballot_sync(~0u, i < n && u > prefix), e = __ballot_sync(~0u, i < n && u == prefix);
+      const uint32_t u = 32 * q < rem ? pk[32 * q] >> shift : 0u;
+      const uint32_t g = __ballot_sync(~0u, u > prefix), e = __ballot_sync(~0u, u == prefix);
       if (lane == q) mg = g, me = e;
     }
+    auto first_bits = [](int k) { return k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u; };
+    vm = lane < groups ? first_bits(n - g0 - 32 * lane) : 0u;
+    lm = first_bits(left - t0 - g0 - 32 * lane);
+    me &= vm;  // slots past the end count as keys of 0
   };
   for (int t0 = lo; t0 < hi; t0 += TILE) {
     const int n = min(TILE, hi - t0);
     if (!one) {
       __syncthreads();
-      load(t0, n);
-      __syncthreads();
+      load(t0, n, false);
     }
-    marks(n);
-    // slots of the lane's group that lie below the new length
-    const int in = min(32, max(0, left - (t0 + g0 + 32 * lane)));
-    const uint32_t lm = in == 32 ? ~0u : (1u << in) - 1u;
+    __syncthreads();
+    marks(t0, n);
     const uint32_t gt = __reduce_add_sync(~0u, __popc(mg)), eq = __reduce_add_sync(~0u, __popc(me));
     const uint32_t gt_l = __reduce_add_sync(~0u, __popc(mg & lm)), eq_l = __reduce_add_sync(~0u, __popc(me & lm));
     if (lane == 0) {
@@ -301,71 +353,59 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
   uint32_t gt_before, eq_before, kept_l;  // before this CTA; kept below the new length
   {
     uint4 t = make_uint4(0, 0, 0, 0);
-    if (lane < C) t = *reinterpret_cast<const uint4*>(C == 1 ? s_tot : cl.map_shared_rank(s_tot, lane));
+    if (lane < C) t = *reinterpret_cast<const uint4*>(SOLO ? s_tot : cl.map_shared_rank(s_tot, lane));
     gt_before = __reduce_add_sync(~0u, lane < rank ? t.x : 0u);
     eq_before = __reduce_add_sync(~0u, lane < rank ? t.y : 0u);
     kept_l = __reduce_add_sync(~0u, t.z) + min(need, __reduce_add_sync(~0u, t.w));
   }
-  if (C > 1) cl.sync();  // no CTA leaves while another still reads its totals
+  if (!SOLO) cl.sync();  // no CTA leaves while another still reads its totals
   if (rank == 0 && tid == 0) p.ws.count[job] = p.budget - (int32_t)kept_l;
   int32_t* dst = p.ws.dst + (int64_t)job * p.ws.moves;
   int32_t* src = p.ws.src + (int64_t)job * p.ws.moves;
+  const uint32_t below = (1u << lane) - 1u;
   for (int t0 = lo; t0 < hi; t0 += TILE) {
     const int n = min(TILE, hi - t0);
     if (!one) {
       __syncthreads();
-      load(t0, n);
+      load(t0, n, false);
       __syncthreads();
-      marks(n);
+      marks(t0, n);
       const uint32_t gt = __reduce_add_sync(~0u, __popc(mg)), eq = __reduce_add_sync(~0u, __popc(me));
       if (lane == 0) s_cnt[warp] = make_uint2(gt, eq);
       __syncthreads();
     }
-    uint32_t g = gt_before, e = eq_before;
-    for (int w = 0; w < WARPS; ++w) {
-      const uint2 c = s_cnt[w];
-      if (w < warp) g += c.x, e += c.y;
-      gt_before += c.x, eq_before += c.y;
-    }
+    const uint2 c = lane < WARPS ? s_cnt[lane] : make_uint2(0, 0);
     // keys above and at the bar before the lane's group
-    g += scan_warp(__popc(mg), lane) - __popc(mg);
-    e += scan_warp(__popc(me), lane) - __popc(me);
-    for (int q0 = 0; q0 < groups; q0 += 4) {
-      float a[4];
-      int b[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = g0 + 32 * (q0 + k) + lane, j = t0 + i;
-        if (q0 + k < groups && i < n && j < left) {
-          if (copy_s) a[k] = sc[j];
-          if (copy_p) b[k] = po[j];
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int q = q0 + k;  // below 32: groups <= 32
-        const uint32_t gm = __shfl_sync(~0u, mg, q), em = __shfl_sync(~0u, me, q);
-        const uint32_t eb = __shfl_sync(~0u, e, q) + __popc(em & below);                      // equal keys before the slot
-        const uint32_t kb = __shfl_sync(~0u, g, q) + __popc(gm & below) + min(need, eb);      // kept slots before it
-        const bool kept = (gm >> lane & 1u) || ((em >> lane & 1u) && eb < need);
-        const int i = g0 + 32 * q + lane, j = t0 + i;
-        if (q < groups && i < n) {
-          if (j < left) {
-            if (!kept) {
-              dst[j - kb] = j;
-            } else {
-              if (copy_s) p.score_out[row + j] = a[k];
-              if (copy_p) p.pos_out[row + j] = b[k];
-            }
-          } else if (kept) {
-            src[kb - kept_l] = j;  // its score and position move with the row
-          } else {
-            p.score_out[row + j] = 0.0f;
-            p.pos_out[row + j] = -1;
-          }
-        }
-      }
+    const uint32_t g = gt_before + __reduce_add_sync(~0u, lane < warp ? c.x : 0u) + scan_warp(__popc(mg), lane) - __popc(mg);
+    const uint32_t e = eq_before + __reduce_add_sync(~0u, lane < warp ? c.y : 0u) + scan_warp(__popc(me), lane) - __popc(me);
+    gt_before += __reduce_add_sync(~0u, c.x);
+    eq_before += __reduce_add_sync(~0u, c.y);
+    const uint32_t kept = mg | lowest_bits(me, need > e ? min(need - e, 32u) : 0u);
+    const uint32_t kb = g + min(need, e);  // kept before the lane's group
+    const uint32_t holes = ~kept & vm & lm, movers = kept & ~lm, gone = ~kept & vm & ~lm;
+    const int j0 = t0 + g0;
+    const int at_h = j0 + 32 * lane - (int)kb, at_m = max(0, (int)(kb - kept_l));
+    for (uint32_t todo = __ballot_sync(~0u, holes != 0); todo; todo &= todo - 1) {
+      const int q = __ffs(todo) - 1;
+      const uint32_t m = __shfl_sync(~0u, holes, q);
+      const int at = __shfl_sync(~0u, at_h, q);
+      if (m >> lane & 1u) dst[at + __popc(m & below)] = j0 + 32 * q + lane;
     }
+    for (uint32_t todo = __ballot_sync(~0u, movers != 0); todo; todo &= todo - 1) {
+      const int q = __ffs(todo) - 1;
+      const uint32_t m = __shfl_sync(~0u, movers, q);
+      const int at = __shfl_sync(~0u, at_m, q);
+      // a mover's score and position move with its row
+      if (m >> lane & 1u) src[at + __popc(m & below)] = j0 + 32 * q + lane;
+    }
+    if (!copy_s || !copy_p)
+      for (uint32_t todo = __ballot_sync(~0u, gone != 0); todo; todo &= todo - 1) {
+        const int q = __ffs(todo) - 1;
+        if (__shfl_sync(~0u, gone, q) >> lane & 1u) {
+          so[j0 + 32 * q + lane] = 0.0f;
+          qo[j0 + 32 * q + lane] = -1;
+        }
+      }
   }
 }
 
@@ -494,14 +534,14 @@ cudaError_t launch_kv_evict(const mf_kv_evict_desc& d, const KvEvictWs& ws, uint
   while (C < EV_CLUSTER && (int64_t)C * EV_SLOTS < d.kv.max_len) C *= 2;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = wide ? allow_smem<&k_evict_select<EV_WIDE>>(dev, 4 * 32 * EV_WIDE)
-                                 : allow_smem<&k_evict_select<EV_THR>>(dev, 4 * 32 * EV_THR);
+  if (e == cudaSuccess) e = wide ? allow_smem<&k_evict_select<EV_WIDE, false>>(dev, 4 * 32 * EV_WIDE)
+                                 : allow_smem<&k_evict_select<EV_THR, false>>(dev, 4 * 32 * EV_THR);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3((unsigned)((int64_t)jobs * C));
   cfg.blockDim = dim3(wide ? EV_WIDE : EV_THR);
-  cfg.dynamicSmemBytes = 4 * (size_t)std::min<int64_t>(most, ((int64_t)d.kv.max_len + C - 1) / C);
+  cfg.dynamicSmemBytes = (4 * (size_t)std::min<int64_t>(most, ((int64_t)d.kv.max_len + C - 1) / C) + 15) & ~size_t(15);
   cfg.stream = st;
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)C;
@@ -509,7 +549,10 @@ cudaError_t launch_kv_evict(const mf_kv_evict_desc& d, const KvEvictWs& ws, uint
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  e = wide ? cudaLaunchKernelEx(&cfg, k_evict_select<EV_WIDE>, p) : cudaLaunchKernelEx(&cfg, k_evict_select<EV_THR>, p);
+  // (a lone CTA holds EV_SLOTS keys at most, which need no raised limit)
+  e = wide ? cudaLaunchKernelEx(&cfg, k_evict_select<EV_WIDE, false>, p)
+      : C > 1 ? cudaLaunchKernelEx(&cfg, k_evict_select<EV_THR, false>, p)
+              : cudaLaunchKernelEx(&cfg, k_evict_select<EV_THR, true>, p);
   if (e != cudaSuccess) return e;
 
   const int chunks = (int)std::max<int64_t>(1, (ws.moves + MV_ROWS - 1) / MV_ROWS);
