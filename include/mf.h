@@ -527,9 +527,10 @@ mf_status mf_kv_evict(const mf_kv_evict_desc* desc, void* workspace, size_t work
  *   score[s][g][j] = sum over heads r of group g, queries j <= i < L_s of P_r[i][j],  j < L_s.
  * Sequence s has L_s = cu_seqlens[s+1] - cu_seqlens[s] tokens and the BSR rows qblock_base[s] ..
  * + ceil(L_s / B) - 1.  Entries with j > i or i, j >= L_s are never used; slots j >= L_s are left
- * as they were.  Column sums and head mix in float32, query blocks added in float64 in ascending
- * order: repeated calls give the same bits.  A BSR row, column or length out of range sets status
- * bit 1 and its blocks are skipped.
+ * as they were.  Column sums and head mix in float32, blocks added in float64 in a fixed order:
+ * repeated calls give the same bits.  A BSR row, column or length out of range sets status bit 1
+ * and its blocks are skipped.  Two sequences may name the same BSR rows if they are equally long;
+ * otherwise bit 1 is set and the blocks of rows that they hold differently are skipped.
  * Requirements: B in {32, 64, 128}; 1 <= h_s <= 256; h_r a multiple of h_kv, h_kv <= 64; values
  * 16-byte aligned; at most 4096 query blocks per sequence; nseq <= 4096; n_rows < 2^24. */
 typedef struct {

@@ -629,3 +629,43 @@ def test_receiver_decodes_after_reused_prefill():
         assert torch.equal(score.cpu(), hscore) and torch.equal(pos.cpu(), hpos)
         assert torch.equal(kv.K.cpu(), c.K) and torch.equal(kv.V.cpu(), c.V)
     _clean(mf)
+
+
+def test_key_scores_of_shared_rows():
+    """Two sequences over the same rows of the maps: equally long they both get the scores; where
+    they disagree on what a row holds it is reported, and no kept entry past an end is used."""
+    mf = _mf()
+    values, row_ptr, cols, base = ref.make_bsr((200,), 64, 4, BF, seed=1)
+    bsr = mf.BSR(row_ptr.cuda(), cols.cuda(), values.cuda(), row_ptr[-1:].cuda())
+    W = torch.rand(2, 4, generator=torch.Generator().manual_seed(1))
+    b = torch.tensor([0, 0], dtype=torch.int32, device="cuda")
+    score = mf.mf_map_key_scores(bsr, W.cuda(), torch.tensor([0, 200, 400], dtype=torch.int32, device="cuda"), b, 200, 1)
+    _clean(mf)
+    want, mag = ref.key_scores(values, row_ptr, cols, W, (200,), base, 64, 1)
+    tol = (64 + 4 + 2 + 8) * 2.0 ** -23 * mag + 1e-30
+    for s in range(2):
+        assert ((score[s].double().cpu() - want[0]).abs() <= tol[0]).all()
+    mf.mf_map_key_scores(bsr, W.cuda(), torch.tensor([0, 200, 390], dtype=torch.int32, device="cuda"), b, 200, 1)
+    assert mf.mf_get_status() == (mf.MF_ERR_DEVICE_INDEX, 1)
+
+
+def test_key_scores_without_blocks():
+    """No rows, no kept blocks, no tokens."""
+    mf = _mf()
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    empty = torch.zeros(0, 2, 32, 32, device="cuda")
+    W = torch.ones(2, 2, device="cuda")
+    cu = torch.tensor([0, 0], dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for top in (0, 40):
+        score = torch.full((1, 1, 40), 2.0, device="cuda")
+        mf.mf_map_key_scores(mf.BSR(zero, none, empty, zero), W, cu, zero, top, 1, score=score)
+        _clean(mf)
+        assert (score == 2.0).all()
+    # rows without a kept block: the keys gathered nothing
+    score = torch.full((1, 1, 45), 2.0, device="cuda")
+    rows = torch.zeros(3, dtype=torch.int32, device="cuda")
+    mf.mf_map_key_scores(mf.BSR(rows, none, empty, zero), W, torch.tensor([0, 40], dtype=torch.int32, device="cuda"), zero, 40, 1,
+                         score=score)
+    _clean(mf)
+    assert (score[..., :40] == 0).all() and (score[..., 40:] == 2.0).all()
