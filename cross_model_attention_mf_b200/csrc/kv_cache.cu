@@ -153,10 +153,10 @@ __device__ __forceinline__ uint32_t lowest_bits(uint32_t m, uint32_t n) {
 template <int THR, bool SOLO>
 __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_constant__ EvictParams p) {
   constexpr int WARPS = THR / 32, TILE = THR * 32, OWN = BINS / THR;
-  static_assert(OWN % 4 == 0, "");
+  static_assert(OWN % 4 == 0 && 32 % OWN == 0 && BINS == 64 * 32, "two levels of the walk");
   extern __shared__ __align__(16) uint32_t s_key[];
   __shared__ __align__(16) uint32_t s_hist[2][BINS];
-  __shared__ uint32_t s_scan[2][WARPS];
+  __shared__ __align__(8) uint32_t s_coarse[2][64];
   __shared__ uint32_t s_pick[2][3];           // bin of the smallest kept key, keys to take from it, keys in it
   __shared__ uint2 s_cnt[WARPS];              // keys above and at the bar, per warp of the tile
   __shared__ __align__(16) uint32_t s_tot[4]; // of the CTA: above, at the bar; and of those, below the new length
@@ -268,41 +268,48 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
         }
       }
     }
-    sync();
-    // every CTA adds up the cluster's histograms and walks them from the top: thread t owns OWN
-    // bins, thread 0 the highest
-    const int b0 = BINS - (tid + 1) * OWN;
-    uint32_t c[OWN];
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) c[i] = 0;
-#pragma unroll 4
-    for (int r = 0; r < C; ++r) {
-      const uint32_t* from = SOLO ? hist : cl.map_shared_rank(hist, r);
+    __syncthreads();
+    // sums of 32 neighbouring bins: thread t adds up OWN of them
+    {
+      uint32_t sum = 0;
 #pragma unroll
       for (int i = 0; i < OWN; i += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(from + b0 + i);
-        c[i] += v.x, c[i + 1] += v.y, c[i + 2] += v.z, c[i + 3] += v.w;
+        const uint4 v = *reinterpret_cast<const uint4*>(hist + tid * OWN + i);
+        sum += v.x + v.y + v.z + v.w;
       }
+#pragma unroll
+      for (int o = 1; o < 32 / OWN; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      if (tid % (32 / OWN) == 0) s_coarse[buf][tid / (32 / OWN)] = sum;
     }
-    uint32_t sum = 0;
+    sync();
+    // The cluster's histograms are walked from the top: by one warp, 64 sums, then 32 bins
+    if (warp == 0) {
+      uint2 two = make_uint2(0, 0);  // sums 63 - 2 lane and 62 - 2 lane
 #pragma unroll
-    for (int i = 0; i < OWN; ++i) sum += c[i];
-    const uint32_t incl = scan_warp(sum, lane);
-    if (lane == 31) s_scan[buf][warp] = incl;
-    if (round == 1)  // the first histogram has been read everywhere: it serves the third round
-      for (int i = tid; i < BINS / 4; i += THR) reinterpret_cast<uint4*>(s_hist[0])[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    uint32_t above = incl - sum + __reduce_add_sync(~0u, lane < warp ? s_scan[buf][lane] : 0u);
-    if (above < need && need <= above + sum) {
-#pragma unroll
-      for (int i = OWN - 1; i >= 0; --i) {
-        if (above < need && need <= above + c[i]) {
-          s_pick[buf][0] = (uint32_t)(b0 + i);
-          s_pick[buf][1] = need - above;
-          s_pick[buf][2] = c[i];
+      for (int r = 0; r < (SOLO ? 1 : EV_CLUSTER); ++r)
+        if (r < C) {
+          const uint32_t* from = SOLO ? s_coarse[buf] : cl.map_shared_rank(s_coarse[buf], r);
+          const uint2 v = *reinterpret_cast<const uint2*>(from + 62 - 2 * lane);
+          two.x += v.y, two.y += v.x;
         }
-        above += c[i];
+      uint32_t above = scan_warp(two.x + two.y, lane) - two.x - two.y;
+      const bool here = above < need && need <= above + two.x + two.y;
+      const int from_lane = __ffs(__ballot_sync(~0u, here)) - 1;
+      const bool second = need > above + two.x;
+      above = __shfl_sync(~0u, second ? above + two.x : above, from_lane);
+      const int coarse = __shfl_sync(~0u, 63 - 2 * lane - (second ? 1 : 0), from_lane);
+      uint32_t c = 0;  // bin 31 - lane of the 32
+#pragma unroll
+      for (int r = 0; r < (SOLO ? 1 : EV_CLUSTER); ++r)
+        if (r < C) c += (SOLO ? hist : cl.map_shared_rank(hist, r))[32 * coarse + 31 - lane];
+      above += scan_warp(c, lane) - c;
+      if (above < need && need <= above + c) {
+        s_pick[buf][0] = (uint32_t)(32 * coarse + 31 - lane);
+        s_pick[buf][1] = need - above;
+        s_pick[buf][2] = c;
       }
+    } else if (round == 1) {  // the first histogram has been read everywhere: it serves the third round
+      for (int i = tid - 32; i < BINS / 4; i += THR - 32) reinterpret_cast<uint4*>(s_hist[0])[i] = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
     prefix = (prefix << (top - shift)) | s_pick[buf][0];
@@ -313,9 +320,9 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
 
   uint32_t mg = 0, me = 0;      // marks of this lane's group: above the bar, at it
   uint32_t lm = 0, vm = 0;      // its slots below the new length, its slots
-  int g0 = 0;                   // the warp's first slot
+  int g0 = 0, groups = 0;       // the warp's first slot, its groups
   auto marks = [&](int t0, int n) {
-    const int groups = (n + THR - 1) / THR;
+    groups = (n + THR - 1) / THR;
     g0 = warp * groups * 32;
     const uint32_t* pk = s_key + g0 + lane;
     const int rem = n - g0 - lane;
@@ -358,7 +365,7 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
     eq_before = __reduce_add_sync(~0u, lane < rank ? t.y : 0u);
     kept_l = __reduce_add_sync(~0u, t.z) + min(need, __reduce_add_sync(~0u, t.w));
   }
-  if (!SOLO) cl.sync();  // no CTA leaves while another still reads its totals
+  if (!SOLO) cl.barrier_arrive();  // no CTA leaves while another still reads its totals: awaited below
   if (rank == 0 && tid == 0) p.ws.count[job] = p.budget - (int32_t)kept_l;
   int32_t* dst = p.ws.dst + (int64_t)job * p.ws.moves;
   int32_t* src = p.ws.src + (int64_t)job * p.ws.moves;
@@ -385,28 +392,21 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
     const uint32_t holes = ~kept & vm & lm, movers = kept & ~lm, gone = ~kept & vm & ~lm;
     const int j0 = t0 + g0;
     const int at_h = j0 + 32 * lane - (int)kb, at_m = max(0, (int)(kb - kept_l));
-    for (uint32_t todo = __ballot_sync(~0u, holes != 0); todo; todo &= todo - 1) {
-      const int q = __ffs(todo) - 1;
-      const uint32_t m = __shfl_sync(~0u, holes, q);
-      const int at = __shfl_sync(~0u, at_h, q);
-      if (m >> lane & 1u) dst[at + __popc(m & below)] = j0 + 32 * q + lane;
-    }
-    for (uint32_t todo = __ballot_sync(~0u, movers != 0); todo; todo &= todo - 1) {
-      const int q = __ffs(todo) - 1;
-      const uint32_t m = __shfl_sync(~0u, movers, q);
-      const int at = __shfl_sync(~0u, at_m, q);
-      // a mover's score and position move with its row
-      if (m >> lane & 1u) src[at + __popc(m & below)] = j0 + 32 * q + lane;
-    }
-    if (!copy_s || !copy_p)
-      for (uint32_t todo = __ballot_sync(~0u, gone != 0); todo; todo &= todo - 1) {
-        const int q = __ffs(todo) - 1;
-        if (__shfl_sync(~0u, gone, q) >> lane & 1u) {
-          so[j0 + 32 * q + lane] = 0.0f;
-          qo[j0 + 32 * q + lane] = -1;
-        }
+    const bool clear = !copy_s || !copy_p;  // the first pass did it otherwise
+#pragma unroll 4
+    for (int q = 0; q < groups; ++q) {
+      const uint32_t mh = __shfl_sync(~0u, holes, q), mm = __shfl_sync(~0u, movers, q);
+      const int ah = __shfl_sync(~0u, at_h, q), am = __shfl_sync(~0u, at_m, q);
+      const int j = j0 + 32 * q + lane;
+      if (mh >> lane & 1u) dst[ah + __popc(mh & below)] = j;
+      if (mm >> lane & 1u) src[am + __popc(mm & below)] = j;  // its score and position move with the row
+      if (clear && (__shfl_sync(~0u, gone, q) >> lane & 1u)) {
+        so[j] = 0.0f;
+        qo[j] = -1;
       }
+    }
   }
+  if (!SOLO) cl.barrier_wait();
 }
 
 // ------------------------------------------------------------------ eviction: moves
