@@ -157,11 +157,9 @@ struct CoreBf16 {
     const uint32_t sring = smem_u32(ring);
     const int64_t hoff = (int64_t)u.hk * kv.row_bytes;
     // byte offset of key row `lane` (< 16) of the k-th tile, -1 past the end
-    auto rows_of = [&](int k) -> int64_t {
-      const int key = (first + k * WARPS) * TK + (lane & 15);
-      if (k >= n_my || key >= u.len) return -1;
-      return kv_slot(kv, u.s, key);
-    };
+    auto key_of = [&](int k) { return (first + k * WARPS) * TK + (lane & 15); };
+    auto held = [&](int k) { return k < n_my && key_of(k) < u.len; };
+    auto rows_of = [&](int k) -> int64_t { return held(k) ? kv_slot(kv, u.s, key_of(k)) : -1; };
     auto issue = [&](int stage, int64_t off) {
       const uint32_t base = sring + stage * TILE;
 #pragma unroll
@@ -176,12 +174,16 @@ struct CoreBf16 {
         cp16(dst + TK * DP * ESZ, kv.V + a, ok ? 16u : 0u);
       }
     };
+    // the first tiles' pages are looked up together
+    int page[STAGES];
+#pragma unroll
+    for (int k = 0; k < STAGES; ++k) page[k] = held(k) ? kv_page(kv, u.s, key_of(k)) : 0;
 #pragma unroll
     for (int k = 0; k < STAGES - 1; ++k) {
-      if (k < n_my) issue(k, rows_of(k));
+      if (k < n_my) issue(k, held(k) ? kv_offset(kv, page[k], key_of(k)) : -1);
       cp_commit();
     }
-    int64_t next = rows_of(STAGES - 1);
+    int64_t next = held(STAGES - 1) ? kv_offset(kv, page[STAGES - 1], key_of(STAGES - 1)) : -1;
     int stage = 0, fill = STAGES - 1;
     float* S = p.S ? p.S + ((int64_t)u.s * p.h_kv + u.hk) * kv.max_len * p.GP : nullptr;
     const int hg = u.h0 - u.hk * p.G;  // first head within the group
@@ -341,11 +343,9 @@ struct CoreF32 {
     const int n_my = first < u.t1 ? (u.t1 - first + WARPS - 1) / WARPS : 0;
     const uint32_t sring = smem_u32(ring);
     const int64_t hoff = (int64_t)u.hk * kv.row_bytes;
-    auto rows_of = [&](int k) -> int64_t {
-      const int key = (first + k * WARPS) * TK + (lane & 7);
-      if (k >= n_my || key >= u.len) return -1;
-      return kv_slot(kv, u.s, key);
-    };
+    auto key_of = [&](int k) { return (first + k * WARPS) * TK + (lane & 7); };
+    auto held = [&](int k) { return k < n_my && key_of(k) < u.len; };
+    auto rows_of = [&](int k) -> int64_t { return held(k) ? kv_slot(kv, u.s, key_of(k)) : -1; };
     auto issue = [&](int stage, int64_t off) {
       const uint32_t base = sring + stage * TILE;
 #pragma unroll
@@ -360,12 +360,16 @@ struct CoreF32 {
         cp16(dst + TK * DP * ESZ, kv.V + a, ok ? 16u : 0u);
       }
     };
+    // the first tiles' pages are looked up together
+    int page[STAGES];
+#pragma unroll
+    for (int k = 0; k < STAGES; ++k) page[k] = held(k) ? kv_page(kv, u.s, key_of(k)) : 0;
 #pragma unroll
     for (int k = 0; k < STAGES - 1; ++k) {
-      if (k < n_my) issue(k, rows_of(k));
+      if (k < n_my) issue(k, held(k) ? kv_offset(kv, page[k], key_of(k)) : -1);
       cp_commit();
     }
-    int64_t next = rows_of(STAGES - 1);
+    int64_t next = held(STAGES - 1) ? kv_offset(kv, page[STAGES - 1], key_of(STAGES - 1)) : -1;
     int stage = 0, fill = STAGES - 1;
     float* S = p.S ? p.S + ((int64_t)u.s * p.h_kv + u.hk) * kv.max_len * p.GP : nullptr;
     const int hg = u.h0 - u.hk * p.G;
@@ -495,8 +499,8 @@ __device__ inline void scan_tiles(const KvView& kv, int tk, int32_t* pre, bool r
   __syncthreads();
 }
 
-__device__ __forceinline__ int64_t tiles_per_cta(int64_t total, int grid) {
-  const int64_t per = (total + grid - 1) / grid;
+template <typename N> __device__ __forceinline__ N tiles_per_cta(N total, int grid) {
+  const N per = total / grid + (total % grid != 0);
   return per < MIN_TILES ? MIN_TILES : per;
 }
 
@@ -610,10 +614,14 @@ struct Parts {
 
 __device__ __forceinline__ Parts unit_parts(const DecodeParams& p, int s, int ui) {
   if (p.whole) return {0, 1};
-  const int64_t total = (int64_t)p.pre[p.kv.nseq] * p.U;
+  const int all = p.pre[p.kv.nseq], before = p.pre[s], nt = p.pre[s + 1] - before;
+  const int64_t total = (int64_t)all * p.U, at = (int64_t)before * p.U + (int64_t)ui * nt;
+  if (total >> 32 == 0) {  // a 64-bit division takes four times the instructions
+    const uint32_t per = (uint32_t)tiles_per_cta((uint32_t)total, p.grid);
+    const uint32_t c0 = (uint32_t)at / per;
+    return {(int64_t)c0, (int)(((uint32_t)at + (uint32_t)nt - 1u) / per - c0) + 1};
+  }
   const int64_t per = tiles_per_cta(total, p.grid);
-  const int nt = p.pre[s + 1] - p.pre[s];
-  const int64_t at = (int64_t)p.pre[s] * p.U + (int64_t)ui * nt;
   const int64_t c0 = at / per;
   return {c0, (int)((at + nt - 1) / per - c0) + 1};
 }
@@ -635,74 +643,118 @@ __device__ __forceinline__ float2 join_stats(const DecodeParams& p, const Parts&
   return make_float2(mu, L);
 }
 
-// sum over the group's heads of 2^(x - lse2), V heads to a load
+// sum of 2^(x - lse2) over the first n of V heads (the others are padding); an empty row, of x = -inf
+// and any lse2, adds 0
 template <int V>
-__device__ __forceinline__ float key_weight(const float* x, const float* lse2, int GP) {
+__device__ __forceinline__ float weights(const float (&x)[V], const float* lse2, int n) {
   float sum = 0.0f;
-  for (int h = 0; h < GP; h += V) {
-    float v[V];
-    if (V == 4) {
-      const float4 t = __ldcs(reinterpret_cast<const float4*>(x + h));
-      v[0] = t.x, v[1] = t.y, v[V - 2] = t.z, v[V - 1] = t.w;
-    } else {
-      const float2 t = __ldcs(reinterpret_cast<const float2*>(x + h));
-      v[0] = t.x, v[1] = t.y;
-    }
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += lse2[h + i] == INFINITY ? 0.0f : ex2(v[i] - lse2[h + i]);
-  }
+  for (int i = 0; i < V; ++i)
+    if (i < n) sum += ex2(x[i] - lse2[i]);
   return sum;
 }
-
-template <int V>
-__device__ __forceinline__ void add_weights(const DecodeParams& p, int64_t row, int j0, int j1, const float* lse2) {
-  const float* S = p.S + row * p.kv.max_len * p.GP;
-  const float* in = p.score_in ? p.score_in + row * p.score_stride : nullptr;
-  float* out = p.score_out + row * p.score_stride;
-  constexpr int UN = 4;
-  for (int j = j0 + threadIdx.x; j < j1; j += UN * JOIN_THR) {
-    float old[UN], w[UN];
-#pragma unroll
-    for (int i = 0; i < UN; ++i) old[i] = in && j + i * JOIN_THR < j1 ? in[j + i * JOIN_THR] : 0.0f;
-#pragma unroll
-    for (int i = 0; i < UN; ++i)
-      w[i] = j + i * JOIN_THR < j1 ? key_weight<V>(S + (int64_t)(j + i * JOIN_THR) * p.GP, lse2, p.GP) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < UN; ++i)
-      if (j + i * JOIN_THR < j1) out[j + i * JOIN_THR] = old[i] + w[i];
+template <int V> __device__ __forceinline__ void load_x(const float* x, float (&v)[V]) {
+  if (V == 4) {
+    const float4 t = __ldcs(reinterpret_cast<const float4*>(x));
+    v[0] = t.x, v[1] = t.y, v[V - 2] = t.z, v[V - 1] = t.w;
+  } else {
+    const float2 t = __ldcs(reinterpret_cast<const float2*>(x));
+    v[0] = t.x, v[1] = t.y;
   }
 }
 
-// The first `joiners` CTAs add up the parts of the units that were cut, a query head at a time:
-// the threads take 16 bytes of the row each, the parts in slices that are added up in order.  The
-// others, one per (key chunk, sequence, key head), turn the x_j into weights and add them up over
-// the group.  Both find the row's lse from the parts' (m, l), lanes over parts.
-__global__ void __launch_bounds__(JOIN_THR) k_decode_join(const __grid_constant__ DecodeParams p, int HT, int joiners) {
-  __shared__ float s_lse2[256 + 4];
+// Keys j0 .. j1 of one row: the group's weights, V heads to a load.  A thread's first loads go out
+// before `ready` has found lse2 (shared memory).
+template <int V, class Ready>
+__device__ __forceinline__ void add_weights(const DecodeParams& p, int64_t row, int j0, int j1, const float* lse2,
+                                            Ready ready) {
+  constexpr int UN = 4;
+  for (int j = j0 + threadIdx.x; j < j1 || j - j0 < JOIN_THR; j += UN * JOIN_THR) {
+    const float* S = p.S + (row * p.kv.max_len + j) * p.GP;
+    const float* in = p.score_in ? p.score_in + row * p.score_stride + j : nullptr;
+    float* out = p.score_out + row * p.score_stride + j;
+    const int rem = j1 - j;
+    float old[UN], x[UN][V];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      old[i] = 0.0f;
+      if (i * JOIN_THR < rem) {
+        if (in) old[i] = in[i * JOIN_THR];
+        load_x<V>(S + i * JOIN_THR * p.GP, x[i]);
+      }
+    }
+    if (j - j0 < JOIN_THR) ready();
+    float sum[UN];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) sum[i] = i * JOIN_THR < rem ? weights<V>(x[i], lse2, p.G) : 0.0f;
+    for (int h = V; h < p.GP; h += V) {
+#pragma unroll
+      for (int i = 0; i < UN; ++i)
+        if (i * JOIN_THR < rem) load_x<V>(S + i * JOIN_THR * p.GP + h, x[i]);
+#pragma unroll
+      for (int i = 0; i < UN; ++i)
+        if (i * JOIN_THR < rem) sum[i] += weights<V>(x[i], lse2 + h, p.G - h);
+    }
+#pragma unroll
+    for (int i = 0; i < UN; ++i)
+      if (i * JOIN_THR < rem) out[i * JOIN_THR] = old[i] + sum[i];
+  }
+}
+
+// a += the parts first, first + step, .. of four columns of head h; part k is scaled to the row's m
+__device__ __forceinline__ void add_parts(const DecodeParams& p, const Parts& u, int HT, int h, float mu, int column,
+                                          int first, int step, float4& a) {
+#pragma unroll 4
+  for (int k = first; k < u.n; k += step) {
+    const int64_t at = u.slot(k) * HT + h;
+    const float f = ex2(p.part_ml[at].x - mu);
+    const float4 v = reinterpret_cast<const float4*>(p.part_O + at * p.d)[column];
+    a.x = fmaf(f, v.x, a.x);
+    a.y = fmaf(f, v.y, a.y);
+    a.z = fmaf(f, v.z, a.z);
+    a.w = fmaf(f, v.w, a.w);
+  }
+}
+__device__ __forceinline__ void write_row(const DecodeParams& p, int row, int column, const float4& a, const float2& ml) {
+  const float inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
+  const int64_t at = (int64_t)row * p.d + 4 * column;
+  if (p.o_f32) *reinterpret_cast<float4*>(p.O + 4 * at) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+  else *reinterpret_cast<uint2*>(p.O + 2 * at) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+  if (column == 0 && p.lse) p.lse[row] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * LN2;
+}
+
+// The first `adders` CTAs, one per (key chunk, sequence, key head), turn the x_j into weights and
+// add them up over the group.  The others add up the parts of the units that were cut: a warp
+// takes a query head, or with `many` parts to a row a CTA does, in slices of the parts that are
+// added up in order.  Both find the row's lse from the parts' (m, l), lanes over parts.
+__global__ void __launch_bounds__(JOIN_THR, 4) k_decode_join(const __grid_constant__ DecodeParams p, int HT, int adders,
+                                                             int many) {
+  __shared__ float s_lse2[256];
   __shared__ float4 s_acc[JOIN_THR];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if ((int)blockIdx.x < joiners) {
-    const int nc = p.d >> 2, ns = JOIN_THR / nc;  // 16-byte columns, slices
-    const int c = tid % nc, sl = tid / nc;
-    for (int r0 = blockIdx.x; r0 < p.kv.nseq * p.h_r; r0 += joiners) {
-      const int s = r0 / p.h_r, r = r0 - s * p.h_r;
+  if ((int)blockIdx.x >= adders) {
+    const int nc = p.d >> 2, ns = JOIN_THR / nc;  // 16-byte columns of a row, slices
+    const int per = many ? 1 : JOIN_THR / 32;     // rows a CTA takes at a time
+    for (int64_t r0 = (int64_t)(blockIdx.x - adders) * per; r0 < (int64_t)p.kv.nseq * p.h_r; r0 += (int64_t)(gridDim.x - adders) * per) {
+      const int row = (int)r0 + (many ? 0 : warp);
+      if (row >= p.kv.nseq * p.h_r) continue;  // a warp on its own: rows of a CTA's are below
+      const int s = row / p.h_r, r = row - s * p.h_r;
       const int hk = r / p.G, b = (r - hk * p.G) / HT, h = r - hk * p.G - b * HT;
       const Parts u = unit_parts(p, s, hk * p.hb + b);
       if (u.n == 1) continue;
       const float2 ml = join_stats(p, u, HT, h, lane);
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (sl < ns)
-#pragma unroll 4
-        for (int k = sl; k < u.n; k += ns) {
-          const int64_t at = u.slot(k) * HT + h;
-          const float f = ex2(p.part_ml[at].x - ml.x);
-          const float4 v = reinterpret_cast<const float4*>(p.part_O + at * p.d)[c];
-          a.x = fmaf(f, v.x, a.x);
-          a.y = fmaf(f, v.y, a.y);
-          a.z = fmaf(f, v.z, a.z);
-          a.w = fmaf(f, v.w, a.w);
+      if (!many) {
+        for (int c = lane; c < nc; c += 32) {
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+          add_parts(p, u, HT, h, ml.x, c, 0, 1, a);
+          write_row(p, row, c, a, ml);
         }
+        continue;
+      }
+      const int c = tid % nc, sl = tid / nc;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (sl < ns) add_parts(p, u, HT, h, ml.x, c, sl, ns, a);
       s_acc[tid] = a;
       __syncthreads();
       if (tid < nc) {
@@ -710,45 +762,36 @@ __global__ void __launch_bounds__(JOIN_THR) k_decode_join(const __grid_constant_
           const float4 v = s_acc[k * nc + tid];
           a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
         }
-        const float inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
-        const int64_t at = (int64_t)r0 * p.d + 4 * tid;
-        if (p.o_f32) {
-          *reinterpret_cast<float4*>(p.O + 4 * at) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-        } else {
-          *reinterpret_cast<uint2*>(p.O + 2 * at) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-        }
-        if (tid == 0 && p.lse) p.lse[r0] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * LN2;
+        write_row(p, row, tid, a, ml);
       }
       __syncthreads();
     }
     return;
   }
-  const int rows = p.kv.nseq * p.h_kv, job = blockIdx.x - joiners;
+  const int rows = p.kv.nseq * p.h_kv, job = blockIdx.x;
   const int chunk = job / rows, sg = job - chunk * rows;
   const int s = sg / p.h_kv, hk = sg - s * p.h_kv;
   const int len = kv_len(p.kv, s, false);
   const int64_t j0 = (int64_t)chunk * JOIN_KEYS;
   if (j0 >= len) return;
-  // lse2 of the group's heads; +inf stands for an empty row and for the padding, whose weights are 0
-  for (int h = warp; h < p.GP; h += JOIN_THR / 32) {
-    float v = INFINITY;
-    if (h < p.G) {
+  auto ready = [&] {  // lse2 of the group's heads (0 for an empty row)
+    for (int h = warp; h < p.G; h += JOIN_THR / 32) {
       const int b = h / HT;
       const Parts u = unit_parts(p, s, hk * p.hb + b);
+      float v;
       if (u.n == 1) {
         v = p.lse2[(int64_t)s * p.h_r + hk * p.G + h];
       } else {
         const float2 ml = join_stats(p, u, HT, h - b * HT, lane);
-        v = ml.y == 0.0f ? -INFINITY : ml.x + log2f(ml.y);
+        v = ml.x + log2f(ml.y);
       }
-      if (v == -INFINITY) v = INFINITY;
+      if (lane == 0) s_lse2[h] = v == -INFINITY ? 0.0f : v;
     }
-    if (lane == 0) s_lse2[h] = v;
-  }
-  __syncthreads();
+    __syncthreads();
+  };
   const int j1 = (int)min((int64_t)len, j0 + JOIN_KEYS);
-  if (p.GP % 4 == 0) add_weights<4>(p, sg, (int)j0, j1, s_lse2);
-  else add_weights<2>(p, sg, (int)j0, j1, s_lse2);
+  if (p.GP % 4 == 0) add_weights<4>(p, sg, (int)j0, j1, s_lse2, ready);
+  else add_weights<2>(p, sg, (int)j0, j1, s_lse2, ready);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -854,9 +897,12 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   if (err != cudaSuccess || (p.whole && !p.score_out)) return err;
 
   cudaLaunchConfig_t cfg{};
-  const int joiners = p.whole ? 0 : std::min(MAX_JOINERS, p.kv.nseq * p.h_r);
+  // parts of a row if all were equally long: from 8 on its join is split over a CTA's warps
+  const int many = p.grid >= 8 * p.kv.nseq * p.U;
+  const int joiners = p.whole ? 0 : std::min(MAX_JOINERS, many ? p.kv.nseq * p.h_r : (p.kv.nseq * p.h_r + 7) / 8);
   const int chunks = p.score_out ? (p.kv.max_len + JOIN_KEYS - 1) / JOIN_KEYS : 0;
-  cfg.gridDim = dim3((unsigned)joiners + (unsigned)chunks * (unsigned)(p.kv.nseq * p.h_kv));
+  const int adders = chunks * p.kv.nseq * p.h_kv;
+  cfg.gridDim = dim3((unsigned)adders + (unsigned)joiners);
   if (cfg.gridDim.x == 0) return cudaSuccess;
   cfg.blockDim = dim3(JOIN_THR);
   cfg.stream = st;
@@ -865,7 +911,7 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_decode_join, p, HT, joiners);
+  return cudaLaunchKernelEx(&cfg, k_decode_join, p, HT, adders, many);
 }
 
 }  // namespace mfi

@@ -62,15 +62,20 @@ __device__ __forceinline__ int kv_len(const KvView& v, int s, bool report) {
   return len < 0 ? 0 : top;
 }
 
-// byte offset (from K or V) of a slot's first head row, -1 for a page id out of range
-__device__ __forceinline__ int64_t kv_slot(const KvView& v, int s, int slot) {
-  const int pg = slot / v.page_size;
-  const int page = v.table[(int64_t)s * v.max_pages + pg];
+// page of a slot of sequence s, as the table has it
+__device__ __forceinline__ int kv_page(const KvView& v, int s, int slot) {
+  return v.table[(int64_t)s * v.max_pages + slot / v.page_size];
+}
+// byte offset (from K or V) of a slot's first head row in that page, -1 for a page id out of range
+__device__ __forceinline__ int64_t kv_offset(const KvView& v, int page, int slot) {
   if (page < 0 || page >= v.n_pages) {
     atomicOr(v.status, ST_PAGE);
     return -1;
   }
-  return (int64_t)page * v.page_bytes + (int64_t)(slot - pg * v.page_size) * v.slot_bytes;
+  return (int64_t)page * v.page_bytes + (int64_t)(slot % v.page_size) * v.slot_bytes;
+}
+__device__ __forceinline__ int64_t kv_slot(const KvView& v, int s, int slot) {
+  return kv_offset(v, kv_page(v, s, slot), slot);
 }
 
 }  // namespace mfi
