@@ -175,15 +175,19 @@ struct CoreBf16 {
       }
     };
     // the first tiles' pages are looked up together
-    int page[STAGES];
+    KvPlace at[STAGES];
+    int id[STAGES];
 #pragma unroll
-    for (int k = 0; k < STAGES; ++k) page[k] = held(k) ? kv_page(kv, u.s, key_of(k)) : 0;
+    for (int k = 0; k < STAGES; ++k) {
+      at[k] = kv_place(kv, held(k) ? key_of(k) : 0);
+      id[k] = held(k) ? kv_page(kv, u.s, at[k]) : 0;
+    }
 #pragma unroll
     for (int k = 0; k < STAGES - 1; ++k) {
-      if (k < n_my) issue(k, held(k) ? kv_offset(kv, page[k], key_of(k)) : -1);
+      if (k < n_my) issue(k, held(k) ? kv_offset(kv, id[k], at[k]) : -1);
       cp_commit();
     }
-    int64_t next = held(STAGES - 1) ? kv_offset(kv, page[STAGES - 1], key_of(STAGES - 1)) : -1;
+    int64_t next = held(STAGES - 1) ? kv_offset(kv, id[STAGES - 1], at[STAGES - 1]) : -1;
     int stage = 0, fill = STAGES - 1;
     float* S = p.S ? p.S + ((int64_t)u.s * p.h_kv + u.hk) * kv.max_len * p.GP : nullptr;
     const int hg = u.h0 - u.hk * p.G;  // first head within the group
@@ -361,15 +365,19 @@ struct CoreF32 {
       }
     };
     // the first tiles' pages are looked up together
-    int page[STAGES];
+    KvPlace at[STAGES];
+    int id[STAGES];
 #pragma unroll
-    for (int k = 0; k < STAGES; ++k) page[k] = held(k) ? kv_page(kv, u.s, key_of(k)) : 0;
+    for (int k = 0; k < STAGES; ++k) {
+      at[k] = kv_place(kv, held(k) ? key_of(k) : 0);
+      id[k] = held(k) ? kv_page(kv, u.s, at[k]) : 0;
+    }
 #pragma unroll
     for (int k = 0; k < STAGES - 1; ++k) {
-      if (k < n_my) issue(k, held(k) ? kv_offset(kv, page[k], key_of(k)) : -1);
+      if (k < n_my) issue(k, held(k) ? kv_offset(kv, id[k], at[k]) : -1);
       cp_commit();
     }
-    int64_t next = held(STAGES - 1) ? kv_offset(kv, page[STAGES - 1], key_of(STAGES - 1)) : -1;
+    int64_t next = held(STAGES - 1) ? kv_offset(kv, id[STAGES - 1], at[STAGES - 1]) : -1;
     int stage = 0, fill = STAGES - 1;
     float* S = p.S ? p.S + ((int64_t)u.s * p.h_kv + u.hk) * kv.max_len * p.GP : nullptr;
     const int hg = u.h0 - u.hk * p.G;
@@ -499,8 +507,8 @@ __device__ inline void scan_tiles(const KvView& kv, int tk, int32_t* pre, bool r
   __syncthreads();
 }
 
-template <typename N> __device__ __forceinline__ N tiles_per_cta(N total, int grid) {
-  const N per = total / grid + (total % grid != 0);
+__device__ __forceinline__ int64_t tiles_per_cta(int64_t total, int grid) {
+  const int64_t per = div_floor(total + grid - 1, grid);
   return per < MIN_TILES ? MIN_TILES : per;
 }
 
@@ -552,7 +560,7 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
     } else {
       const int nt = pre[s + 1] - pre[s];
       const int64_t rel = x - (int64_t)pre[s] * p.U;
-      ui = (int)(rel / nt);
+      ui = (int)div_floor(rel, nt);
       u.t0 = (int)(rel - (int64_t)ui * nt);
       u.t1 = (int)min((int64_t)nt, u.t0 + (end - x));
       begins = u.t0 == 0;
@@ -615,15 +623,10 @@ struct Parts {
 __device__ __forceinline__ Parts unit_parts(const DecodeParams& p, int s, int ui) {
   if (p.whole) return {0, 1};
   const int all = p.pre[p.kv.nseq], before = p.pre[s], nt = p.pre[s + 1] - before;
-  const int64_t total = (int64_t)all * p.U, at = (int64_t)before * p.U + (int64_t)ui * nt;
-  if (total >> 32 == 0) {  // a 64-bit division takes four times the instructions
-    const uint32_t per = (uint32_t)tiles_per_cta((uint32_t)total, p.grid);
-    const uint32_t c0 = (uint32_t)at / per;
-    return {(int64_t)c0, (int)(((uint32_t)at + (uint32_t)nt - 1u) / per - c0) + 1};
-  }
-  const int64_t per = tiles_per_cta(total, p.grid);
-  const int64_t c0 = at / per;
-  return {c0, (int)((at + nt - 1) / per - c0) + 1};
+  const int64_t per = tiles_per_cta((int64_t)all * p.U, p.grid);
+  const int64_t at = (int64_t)before * p.U + (int64_t)ui * nt;
+  const int64_t c0 = div_floor(at, per);
+  return {c0, (int)(div_floor(at + nt - 1, per) - c0) + 1};
 }
 
 // m (0 for an empty row) and l of head h over the parts: one warp, the same in every lane

@@ -27,6 +27,8 @@ struct KvView {
   int32_t slot_bytes;  // h_kv * d * element: one slot's rows of every key head
   int32_t row_bytes;   // d * element: one key head's row
   int n_pages, page_size, max_pages, nseq, max_len;
+  uint32_t page_mul;   // n / page_size = n page_mul >> page_shift, 0 <= n < 2^31
+  int page_shift;
   const int32_t* table;
   const int32_t* lens;
   uint32_t* status;
@@ -42,6 +44,12 @@ inline KvView kv_view(const mf_paged_kv& k, uint32_t* status) {
   v.page_bytes = k.page_stride ? k.page_stride * e : (int64_t)k.page_size * v.slot_bytes;
   v.n_pages = k.n_pages;
   v.page_size = k.page_size;
+  // with 2^l >= page_size and mul = floor(2^(31+l) / page_size) + 1 the product exceeds
+  // n 2^(31+l) / page_size by at most n 2^l / page_size: too little to reach the next quotient
+  int l = 0;
+  while (((int64_t)1 << l) < k.page_size) ++l;
+  v.page_shift = 31 + l;
+  v.page_mul = (uint32_t)((uint64_t(1) << v.page_shift) / (uint64_t)k.page_size + 1);
   v.max_pages = k.max_pages;
   v.nseq = k.nseq;
   v.max_len = k.max_len;
@@ -62,20 +70,35 @@ __device__ __forceinline__ int kv_len(const KvView& v, int s, bool report) {
   return len < 0 ? 0 : top;
 }
 
-// page of a slot of sequence s, as the table has it
-__device__ __forceinline__ int kv_page(const KvView& v, int s, int slot) {
-  return v.table[(int64_t)s * v.max_pages + slot / v.page_size];
+// floor of a / b for a >= 0, b > 0 (a 64-bit division takes four times the instructions)
+__device__ __forceinline__ int64_t div_floor(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
 }
-// byte offset (from K or V) of a slot's first head row in that page, -1 for a page id out of range
-__device__ __forceinline__ int64_t kv_offset(const KvView& v, int page, int slot) {
-  if (page < 0 || page >= v.n_pages) {
+
+// where a slot lies: its page's place in the table, its row in the page
+struct KvPlace {
+  int page, row;
+};
+__device__ __forceinline__ KvPlace kv_place(const KvView& v, int slot) {
+  const int page = (int)(((uint64_t)(uint32_t)slot * v.page_mul) >> v.page_shift);
+  return {page, slot - page * v.page_size};
+}
+// the page id of sequence s in that place
+__device__ __forceinline__ int kv_page(const KvView& v, int s, const KvPlace& at) {
+  return v.table[(int64_t)s * v.max_pages + at.page];
+}
+// byte offset (from K or V) of the slot's first head row in page `id`, -1 for an id out of range
+__device__ __forceinline__ int64_t kv_offset(const KvView& v, int id, const KvPlace& at) {
+  if ((unsigned)id >= (unsigned)v.n_pages) {
     atomicOr(v.status, ST_PAGE);
     return -1;
   }
-  return (int64_t)page * v.page_bytes + (int64_t)(slot % v.page_size) * v.slot_bytes;
+  return (int64_t)id * v.page_bytes + (int64_t)at.row * v.slot_bytes;
 }
 __device__ __forceinline__ int64_t kv_slot(const KvView& v, int s, int slot) {
-  return kv_offset(v, kv_page(v, s, slot), slot);
+  const KvPlace at = kv_place(v, slot);
+  return kv_offset(v, kv_page(v, s, at), at);
 }
 
 }  // namespace mfi
