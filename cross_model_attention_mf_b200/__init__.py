@@ -2,7 +2,7 @@
 
 Argument marshalling only: every step of the path runs in the CUDA kernels of
 libmf.so.  PyTorch supplies device memory and the current stream.  Importing
-this package fails loudly when libmf.so is missing; there is no fallback.
+this package fails loudly when libmf.so or _mf_bind.so is missing; there is no fallback.
 
 Functions mirror the C entry points:
     mf_compress(...)        -> BSR (row_ptr, col_idx, values, nnz)
@@ -38,6 +38,11 @@ if not os.path.exists(LIB_PATH):
                       "(nvcc, sm_100a); this package has no CPU or library fallback")
 
 _lib = ctypes.CDLL(LIB_PATH)
+try:
+    from . import _mf_bind
+except ImportError as e:
+    raise ImportError("_mf_bind.so is missing or does not fit the installed PyTorch: build it with "
+                      "`python -m cross_model_attention_mf_b200.build`") from e
 
 MF_OK, MF_ERR_INVALID, MF_ERR_UNSUPPORTED, MF_ERR_CAPACITY, MF_ERR_CUDA, MF_ERR_TIMEOUT, \
     MF_ERR_DEVICE_INDEX = range(7)
@@ -601,92 +606,10 @@ def choose_sender_layer(residuals_per_candidate: Sequence[torch.Tensor]) -> int:
 
 # ----------------------------------------------------------------------------- paged cache
 
-def _at(t, what, dtype, shape, index, dense=True):
-    """Address of a tensor that is as the call needs it; any other is refused.  A decode step makes
-    these checks for some ten tensors, so the accepted case takes five calls and no more."""
-    try:
-        if t.dtype is dtype and t.get_device() == index >= 0 and t.shape == shape and \
-                (not dense or t.is_contiguous()):
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    raise ValueError(_fault(t, what, dtype, shape, index))
-
-
-def _fault(t, what, dtype, shape, index):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        return f"{what} must be a CUDA tensor"
-    if t.dtype != dtype:
-        return f"{what} must be {dtype}, not {t.dtype}"
-    if t.get_device() != index:
-        return f"{what} is on {t.device}, the call's other tensors on cuda:{index}"
-    if t.shape != shape:
-        return f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}"
-    return f"{what} must be contiguous"
-
-
-def _sizes(t, what, dims):
-    """Shape of a tensor argument with `dims` dimensions."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {dims} dimensions")
-    return t.shape
-
-
-def _row_stride(a, b, what):
-    """Elements between the rows (dim 0) of a and b, which must agree; their other dims must be
-    dense.  0 for dense rows."""
-    if a.is_contiguous() and (b is None or b.is_contiguous()):
-        return 0
-    strides, shape = a.stride(), a.shape
-    if b is not None and b.stride() != strides and shape[0] > 1:
-        raise ValueError(f"{what} must have the same strides")
-    step = 1
-    for n, have in zip(shape[:0:-1], strides[:0:-1]):
-        if have != step and n != 1:
-            raise ValueError(f"{what}: the dims after the first must be dense")
-        step *= n
-    return strides[0] if shape[0] > 1 and step else 0
-
-
-_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() without the Stream object
-
-
-def _on(index, stream):
-    return _raw_stream(index) if stream is None else stream.cuda_stream
-
-
-def _i32(n, what):
-    n = int(n)
-    if not -1 << 31 <= n < 1 << 31:  # ctypes would cut it off
-        raise ValueError(f"{what} = {n} does not fit 32 bits")
-    return n
-
-
-def _new(make, shape, dtype, index, stream):
-    """make (torch.empty or zeros) on the stream that will use the tensor: memory from another
-    stream's pool may still be in use there."""
-    if stream is None:
-        return make(shape, dtype=dtype, device=index)
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=index)
-
-
-def _enqueue(name, d, workspace, index, stream):
-    """Workspace and launch of one call on device `index`, on `stream` or the current one."""
-    if torch.cuda.current_device() != index:
-        with torch.cuda.device(index):
-            return _enqueue(name, d, workspace, index, stream)
-    if workspace is None:
-        need = ctypes.c_size_t(0)
-        _check(getattr(_lib, name + "_workspace_size")(d, need))
-        workspace = _new(torch.empty, max(need.value, 1), torch.uint8, index, stream)
-    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
-    rc = getattr(_lib, name)(d, workspace.data_ptr(), workspace.nbytes, _on(index, stream))
-    if rc:
-        _check(rc)
+# the calls below are made by _mf_bind (csrc/bind.cpp), which checks the tensors and fills the descriptors
+_mf_bind.attach({_n: ctypes.cast(getattr(_lib, _n), _P).value for _n in (
+    "mf_paged_decode", "mf_paged_decode_workspace_size", "mf_kv_append", "mf_kv_evict",
+    "mf_kv_evict_workspace_size", "mf_map_key_scores", "mf_map_key_scores_workspace_size")}, _check)
 
 
 @dataclass
@@ -711,21 +634,7 @@ class PagedKV:
         return self.K.device
 
     def desc(self) -> PagedKVDesc:
-        return self._plan()[0]
-
-    def _plan(self):
-        """Descriptor, device index, dtype, nseq, h_kv and d."""
-        K, V, table = self.K, self.V, self.block_table
-        code, index, shape = _dt(K), K.get_device(), _sizes(K, "K", 4)
-        n_pages, page_size, h_kv, d = shape
-        if n_pages >> 31 or page_size >> 31:
-            raise ValueError("n_pages and page_size must be below 2^31")
-        nseq, max_pages = wide = _sizes(table, "block_table", 2)
-        k, v = _at(K, "K", K.dtype, shape, index, False), _at(V, "V", K.dtype, shape, index, False)
-        return PagedKVDesc(k, v, code, _row_stride(K, V, "pages of K and V"), n_pages, page_size, max_pages,
-                           h_kv, d, _at(table, "block_table", torch.int32, wide, index),
-                           _at(self.seq_lens, "seq_lens", torch.int32, (nseq,), index), nseq,
-                           _i32(self.max_len, "max_len")), index, K.dtype, nseq, h_kv, d
+        return PagedKVDesc.from_buffer_copy(_mf_bind.paged_kv(self))
 
 
 def mf_paged_decode_workspace_size(kv: PagedKV, h_r: int, scores: bool = False) -> int:
@@ -750,27 +659,7 @@ def mf_paged_decode(kv: PagedKV, Q: torch.Tensor, O: Optional[torch.Tensor] = No
     means 1 / sqrt(d).  lse: float32 [nseq, h_r] out.  score float32 [nseq, h_kv, stride]: the
     call's weights are added to it, into score_out when given, else in place; score_out alone
     receives the weights."""
-    kd, index, dtype, nseq, h_kv, d = kv._plan()
-    h_r = _sizes(Q, "Q", 3)[1]
-    shape = (nseq, h_r, d)
-    q = _at(Q, "Q", dtype, shape, index, False)
-    o_type = torch.float32 if o_f32 else dtype
-    if O is None:
-        O = _new(torch.empty, shape, o_type, index, stream)
-    o = _at(O, "O", o_type, shape, index)
-    l = None if lse is None else _at(lse, "lse", torch.float32, (nseq, h_r), index)
-    s_in = s_out = None
-    wide = 0
-    if score is not None or score_out is not None:
-        wide = _sizes(score_out if score is None else score, "score", 3)[2]
-        if score is not None:
-            s_in = s_out = _at(score, "score", torch.float32, (nseq, h_kv, wide), index)
-        if score_out is not None:
-            s_out = _at(score_out, "score_out", torch.float32, (nseq, h_kv, wide), index)
-    _enqueue("mf_paged_decode",
-             PagedDecodeDesc(kd, q, _row_stride(Q, None, "Q"), h_r, float(scale), o, l, s_in, s_out, wide,
-                             MF_DECODE_O_F32 if o_f32 else 0), workspace, index, stream)
-    return O
+    return _mf_bind.paged_decode(kv, Q, O, scale, lse, score, score_out, o_f32, workspace, stream)
 
 
 def mf_kv_append(kv: PagedKV, K_new: torch.Tensor, V_new: torch.Tensor, cu_seqlens_new: torch.Tensor,
@@ -780,27 +669,7 @@ def mf_kv_append(kv: PagedKV, K_new: torch.Tensor, V_new: torch.Tensor, cu_seqle
     """Enqueue the copy of new tokens' K_new, V_new [T, h_kv, d] (rows may be strided) into the
     cache, whose seq_lens already count them; their scores become 0 and their positions
     n_seen - n .. n_seen - 1 where score / pos [nseq, h_kv, stride] are given."""
-    kd, index, dtype, nseq, h_kv, d = kv._plan()
-    T = _sizes(K_new, "K_new", 3)[0]
-    shape = (T, h_kv, d)
-    k, v = _at(K_new, "K_new", dtype, shape, index, False), _at(V_new, "V_new", dtype, shape, index, False)
-    cu = _at(cu_seqlens_new, "cu_seqlens_new", torch.int32, (nseq + 1,), index)
-    seen = None if n_seen is None else _at(n_seen, "n_seen", torch.int32, (nseq,), index)
-    wide, s, p = 0, None, None
-    if score is not None or pos is not None:
-        wide = _sizes(pos if score is None else score, "score", 3)[2]
-        if score is not None:
-            s = _at(score, "score", torch.float32, (nseq, h_kv, wide), index)
-        if pos is not None:
-            p = _at(pos, "pos", torch.int32, (nseq, h_kv, wide), index)
-    desc = KvAppendDesc(kd, k, v, _row_stride(K_new, V_new, "rows of K_new and V_new"), T, cu,
-                        _i32(max_new, "max_new"), seen, s, p, wide)
-    if torch.cuda.current_device() != index:
-        with torch.cuda.device(index):
-            return _check(_lib.mf_kv_append(desc, _on(index, stream)))
-    rc = _lib.mf_kv_append(desc, _on(index, stream))
-    if rc:
-        _check(rc)
+    _mf_bind.kv_append(kv, K_new, V_new, cu_seqlens_new, max_new, n_seen, score, pos, stream)
 
 
 def mf_kv_evict_workspace_size(kv: PagedKV, budget: int) -> int:
@@ -822,21 +691,8 @@ def mf_kv_evict(kv: PagedKV, score: torch.Tensor, pos: torch.Tensor, budget: int
     rows past the budget move into the dropped slots.  score float32 and pos int32
     [nseq, h_kv, stride] follow, in place unless score_out / pos_out are given.  Returns the new
     lengths: seq_lens_out, or kv.seq_lens updated in place."""
-    kd, index, _, nseq, h_kv, _ = kv._plan()
-    wide = _sizes(score, "score", 3)[2]
-    shape = (nseq, h_kv, wide)
-    s_out = s_in = _at(score, "score", torch.float32, shape, index)
-    p_out = p_in = _at(pos, "pos", torch.int32, shape, index)
-    if score_out is not None:
-        s_out = _at(score_out, "score_out", torch.float32, shape, index)
-    if pos_out is not None:
-        p_out = _at(pos_out, "pos_out", torch.int32, shape, index)
-    seen = None if n_seen is None else _at(n_seen, "n_seen", torch.int32, (nseq,), index)
-    out = kv.seq_lens if seq_lens_out is None else seq_lens_out
-    left = _at(out, "seq_lens_out", torch.int32, (nseq,), index)
-    _enqueue("mf_kv_evict", KvEvictDesc(kd, s_in, p_in, s_out, p_out, wide, seen, _i32(budget, "budget"),
-                                        _i32(sink, "sink"), _i32(window, "window"), left), workspace, index, stream)
-    return out
+    return _mf_bind.kv_evict(kv, score, pos, budget, sink, window, n_seen, score_out, pos_out, seq_lens_out,
+                             workspace, stream)
 
 
 def mf_map_key_scores_workspace_size(capacity: int, B: int, h_kv: int) -> int:
@@ -857,24 +713,4 @@ def mf_map_key_scores(bsr: BSR, W: torch.Tensor, cu_seqlens: torch.Tensor, qbloc
     one receiver layer's W float32 [h_r, h_s], one sender layer's BSR.  Returns score float32
     [nseq, h_kv, stride >= max_seqlen] (zeros allocated on the call's stream when None); slots past a sequence's
     length are left as they were."""
-    h_kv, max_seqlen = _i32(h_kv, "h_kv"), _i32(max_seqlen, "max_seqlen")
-    values, row_ptr = bsr.values, bsr.row_ptr
-    code, index = _dt(values), values.get_device()
-    cap, h_s, B, B2 = shape = _sizes(values, "values", 4)
-    rows, h_r = _sizes(row_ptr, "row_ptr", 1), _sizes(W, "W", 2)[0]
-    kept = _sizes(bsr.col_idx, "col_idx", 1)
-    if B2 != B or kept[0] < cap or rows[0] < 1:
-        raise ValueError("values must be [capacity, h_s, B, B], col_idx [capacity], row_ptr [rows + 1]")
-    blocks = BsrDesc(_at(row_ptr, "row_ptr", torch.int32, rows, index),
-                     _at(bsr.col_idx, "col_idx", torch.int32, kept, index),
-                     _at(values, "values", values.dtype, shape, index), cap)
-    nseq = _sizes(cu_seqlens, "cu_seqlens", 1)[0] - 1
-    if score is None:
-        score = _new(torch.zeros, (nseq, h_kv, max(max_seqlen, 1)), torch.float32, index, stream)
-    wide = _sizes(score, "score", 3)[2]
-    d = KeyScoresDesc(blocks, rows[0] - 1, code, h_s, B, _at(W, "W", torch.float32, (h_r, h_s), index), h_r, h_kv,
-                      _at(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), index),
-                      _at(qblock_base, "qblock_base", torch.int32, (nseq,), index), nseq, max_seqlen,
-                      _at(score, "score", torch.float32, (nseq, h_kv, wide), index), wide)
-    _enqueue("mf_map_key_scores", d, workspace, index, stream)
-    return score
+    return _mf_bind.map_key_scores(bsr, W, cu_seqlens, qblock_base, max_seqlen, h_kv, score, workspace, stream)

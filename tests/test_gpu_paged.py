@@ -669,3 +669,99 @@ def test_key_scores_without_blocks():
                          score=score)
     _clean(mf)
     assert (score[..., :40] == 0).all() and (score[..., 40:] == 2.0).all()
+
+
+# ------------------------------------------------------------------ what the binding refuses
+
+def test_binding_refusals():
+    mf = _mf()
+    c, _ = ref.make_cache((40, 20), 2, 64, 16, BF, seed=2, spare=3)
+    kv = _kv(mf, c)
+    Q = torch.zeros(2, 8, 64, dtype=BF, device="cuda")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    score, pos = torch.zeros(2, 2, 40, device="cuda"), torch.zeros(2, 2, 40, dtype=torch.int32, device="cuda")
+    new = torch.zeros(2, 2, 64, dtype=BF, device="cuda")
+
+    def with_kv(**kw):
+        f = dict(K=kv.K, V=kv.V, block_table=kv.block_table, seq_lens=kv.seq_lens, max_len=40)
+        f.update(kw)
+        return mf.PagedKV(**f)
+
+    def no(match, call, error=ValueError):
+        with pytest.raises(error, match=match):
+            call()
+
+    for bad, match in ((dict(V=kv.V[:-1]), "shape"), (dict(V=kv.V.float()), "must be"), (dict(K=kv.K.cpu()), "CUDA"),
+                       (dict(K=kv.K[0]), "dimensions"), (dict(K=kv.K[:, :, :, ::2], V=kv.V[:, :, :, ::2]), "dense"),
+                       (dict(V=torch.cat([kv.V, kv.V], 1)[:, :16]), "same stride"), (dict(seq_lens=i32(1)), "shape"),
+                       (dict(seq_lens=kv.seq_lens.long()), "must be"), (dict(block_table=kv.block_table.t()), "contiguous|shape"),
+                       (dict(max_len=1 << 31), "32 bits"), (dict(K=None), "CUDA")):
+        for call in (lambda: mf.mf_paged_decode(with_kv(**bad), Q), lambda: mf.mf_kv_evict(with_kv(**bad), score, pos, 5),
+                     lambda: mf.mf_kv_append(with_kv(**bad), new, new, i32(0, 1, 2), 1), lambda: with_kv(**bad).desc()):
+            no(match, call)
+    no("dtype", lambda: mf.mf_paged_decode(with_kv(K=kv.K.half(), V=kv.V.half()), Q.half()), TypeError)
+    no("int", lambda: mf.mf_paged_decode(with_kv(max_len="40"), Q), TypeError)
+    no("K", lambda: mf.mf_paged_decode(object(), Q), AttributeError)
+    for args, match in ((dict(Q=Q.float()), "must be"), (dict(Q=Q[:1]), "shape"), (dict(Q=Q[..., :32]), "shape"),
+                        (dict(Q=Q.transpose(1, 2).contiguous().transpose(1, 2)), "dense"), (dict(O=Q.float()), "must be"),
+                        (dict(O=Q[:, ::2]), "shape"), (dict(O=Q, o_f32=True), "must be"), (dict(lse=score), "shape"),
+                        (dict(score=score[:, :, ::2]), "contiguous"), (dict(score=score, score_out=score[:, :, 1:]), "shape|contiguous"),
+                        (dict(score=pos), "must be"), (dict(workspace=torch.empty(9)), "CUDA"),
+                        (dict(workspace=torch.empty(4, 4, device="cuda").t()), "contiguous")):
+        a = dict(Q=Q)
+        a.update(args)
+        no(match, lambda: mf.mf_paged_decode(kv, **a))
+    for args in (dict(Q=Q[:, :7].contiguous()), dict(scale=-1.0), dict(score=torch.zeros(2, 2, 39, device="cuda")),
+                 dict(workspace=torch.empty(16, device="cuda"))):
+        a = dict(Q=Q)
+        a.update(args)
+        no("mf status 1", lambda: mf.mf_paged_decode(kv, **a), mf.MFError)
+    no("shape", lambda: mf.mf_kv_append(kv, new, new[:1], i32(0, 1, 2), 1))
+    no("shape", lambda: mf.mf_kv_append(kv, new, new, i32(0, 1), 1))
+    no("mf status 1", lambda: mf.mf_kv_append(kv, new, new, i32(0, 1, 2), 41), mf.MFError)
+    no("32 bits", lambda: mf.mf_kv_append(kv, new, new, i32(0, 1, 2), -(1 << 40)))
+    no("shape", lambda: mf.mf_kv_evict(kv, score, pos[:, :, 1:], 5))
+    no("32 bits", lambda: mf.mf_kv_evict(kv, score, pos, (1 << 32) + 5))
+    no("mf status 1", lambda: mf.mf_kv_evict(kv, score, pos, 5, 3, 3), mf.MFError)
+    no("int|attribute", lambda: mf.mf_kv_evict(kv, score, pos, 5, stream=7), AttributeError)
+    values, row_ptr, cols, base = ref.make_bsr((40,), 32, 2, BF)
+    bsr = mf.BSR(row_ptr.cuda(), cols.cuda(), values.cuda(), row_ptr[-1:].cuda())
+    W = torch.zeros(4, 2, device="cuda")
+    for args, match in ((dict(W=W[:, :1].contiguous()), "shape"), (dict(W=W.to(BF)), "must be"), (dict(h_kv=0), "h_kv"),
+                        (dict(cu_seqlens=i32()), "cu_seqlens"), (dict(qblock_base=i32(0, 1)), "shape"),
+                        (dict(score=score), "shape"), (dict(max_seqlen=1 << 33), "32 bits"),
+                        (dict(bsr=mf.BSR(row_ptr.cuda(), cols[:1].cuda(), values.cuda(), row_ptr[-1:].cuda())), "capacity")):
+        a = dict(bsr=bsr, W=W, cu_seqlens=i32(0, 40), qblock_base=i32(0), max_seqlen=40, h_kv=2)
+        a.update(args)
+        no(match, lambda: mf.mf_map_key_scores(**a))
+    _clean(mf)
+    assert (score == 0).all() and (pos == 0).all()
+
+
+def test_calls_on_a_stream_that_is_not_current():
+    """Outputs, zeros and workspaces that a call allocates belong to the call's stream: work that is
+    still queued on the current stream does not disturb them."""
+    mf = _mf()
+    c, _ = ref.make_cache((700, 90), 2, 64, 16, BF, seed=31)
+    kv = _kv(mf, c)
+    Q = torch.randn(2, 8, 64, generator=torch.Generator().manual_seed(1)).to(BF)
+    Qd = Q.cuda()
+    values, row_ptr, cols, base = ref.make_bsr((200,), 64, 4, BF, seed=1)
+    bsr = mf.BSR(row_ptr.cuda(), cols.cuda(), values.cuda(), row_ptr[-1:].cuda())
+    W = torch.rand(2, 4, generator=torch.Generator().manual_seed(1))
+    Wd = W.cuda()
+    cu = torch.tensor([0, 200], dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    big = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(8):
+        big = big @ big * 1e-3  # the current stream is busy, and frees what it used
+    O = mf.mf_paged_decode(kv, Qd, stream=side)
+    score = mf.mf_map_key_scores(bsr, Wd, cu, zero, 200, 1, stream=side)
+    side.synchronize()
+    check_decode(c, Q, O)
+    want, mag = ref.key_scores(values, row_ptr, cols, W, (200,), base, 64, 1)
+    assert ((score.double().cpu() - want).abs() <= (64 + 4 + 2 + 8) * 2.0 ** -23 * mag + 1e-30).all()
+    torch.cuda.synchronize()
+    _clean(mf)
