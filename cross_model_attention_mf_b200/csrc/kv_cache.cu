@@ -411,57 +411,68 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
 
 // ------------------------------------------------------------------ eviction: moves
 constexpr int MV_THR = 256;
-constexpr int MV_ROWS = 64;  // moves per CTA
+constexpr int MV_ROWS = 16;                        // rows a warp moves
+constexpr int MV_CHUNK = MV_ROWS * (MV_THR / 32);  // moves per CTA
 
-__global__ void __launch_bounds__(MV_THR) k_evict_move(const __grid_constant__ EvictParams p, int chunks) {
+// A warp looks its rows up together (lanes 0..15 the sources, 16..31 the targets), then copies
+// them, four loads of K and of V on their way in every lane.  The warps need not wait for one
+// another, so that some look up while others copy.
+__global__ void __launch_bounds__(MV_THR, 4) k_evict_move(const __grid_constant__ EvictParams p, int chunks) {
   const int job = blockIdx.x / chunks, chunk = blockIdx.x - job * chunks;
   const int s = job / p.h_kv, g = job - s * p.h_kv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (chunk == 0 && g == 0 && threadIdx.x == 0) p.lens_out[s] = p.ws.len[s];
-  const int n = p.ws.count[job];
-  const int m0 = chunk * MV_ROWS, m1 = min(n, m0 + MV_ROWS);
-  if (m0 >= m1) return;
-  __shared__ int64_t s_src[MV_ROWS], s_dst[MV_ROWS];
-  for (int i = m0 + threadIdx.x; i < m1; i += MV_THR) {
-    const int a = p.ws.src[(int64_t)job * p.ws.moves + i], b = p.ws.dst[(int64_t)job * p.ws.moves + i];
+  const int m0 = chunk * MV_CHUNK + warp * MV_ROWS;
+  const int rows = min(MV_ROWS, p.ws.count[job] - m0);
+  if (rows <= 0) return;
+  const int mine = lane & (MV_ROWS - 1);
+  int slot = 0;
+  int64_t off = -1;
+  if (mine < rows) {
+    slot = (lane < MV_ROWS ? p.ws.src : p.ws.dst)[(int64_t)job * p.ws.moves + m0 + mine];
+    const int64_t at = kv_slot(p.kv, s, slot);
+    if (at >= 0) off = at + (int64_t)g * p.kv.row_bytes;
+  }
+  const int to_slot = __shfl_down_sync(~0u, slot, MV_ROWS);
+  if (lane < rows) {
     const int64_t row = (int64_t)job * p.stride;
-    const float sv = p.score_in[row + a];
-    const int pv = p.pos_in[row + a];
-    p.score_out[row + b] = sv;
-    p.pos_out[row + b] = pv;
-    p.score_out[row + a] = 0.0f;
-    p.pos_out[row + a] = -1;
-    const int64_t off = (int64_t)g * p.kv.row_bytes;
-    const int64_t x = kv_slot(p.kv, s, a), y = kv_slot(p.kv, s, b);
-    s_src[i - m0] = x < 0 ? -1 : x + off;
-    s_dst[i - m0] = y < 0 ? -1 : y + off;
+    const float sv = p.score_in[row + slot];
+    const int pv = p.pos_in[row + slot];
+    p.score_out[row + to_slot] = sv;
+    p.pos_out[row + to_slot] = pv;
+    p.score_out[row + slot] = 0.0f;
+    p.pos_out[row + slot] = -1;
   }
-  __syncthreads();
+  // nv vectors of 16 bytes to a row; short rows are copied several at a time
   const int nv = p.kv.row_bytes >> 4;
-  const int work = (m1 - m0) * nv;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int i0 = threadIdx.x; i0 < work; i0 += 4 * MV_THR) {
-    uint4 k[4], v[4];
-    int64_t to[4];
+  const int together = nv < 32 ? 32 / nv : 1;
+  const int sub = nv < 32 ? lane / nv : 0, col = nv < 32 ? lane - sub * nv : lane;
+  for (int c0 = 0; c0 < nv; c0 += 32)
+    for (int r0 = 0; r0 < rows; r0 += 4 * together) {
+      uint4 k[4], v[4];
+      int64_t to[4];
+      const int c = (c0 + col) * 16;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * MV_THR;
-      to[j] = -1;
-      if (i < work) {
-        const int m = i / nv, c = (i - m * nv) * 16;
-        const int64_t a = s_src[m];
-        k[j] = a >= 0 ? *reinterpret_cast<const uint4*>(p.kv.K + a + c) : zero;
-        v[j] = a >= 0 ? *reinterpret_cast<const uint4*>(p.kv.V + a + c) : zero;
-        if (s_dst[m] >= 0) to[j] = s_dst[m] + c;
+      for (int j = 0; j < 4; ++j) {
+        const int r = r0 + j * together + sub;
+        const int64_t from = __shfl_sync(~0u, off, r & (MV_ROWS - 1));
+        to[j] = __shfl_sync(~0u, off, MV_ROWS + (r & (MV_ROWS - 1)));
+        k[j] = v[j] = make_uint4(0, 0, 0, 0);
+        if (r >= rows || sub >= together || c0 + col >= nv) {
+          to[j] = -1;
+        } else if (from >= 0) {
+          k[j] = *reinterpret_cast<const uint4*>(p.kv.K + from + c);
+          v[j] = *reinterpret_cast<const uint4*>(p.kv.V + from + c);
+        }
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (to[j] >= 0) {
+          *reinterpret_cast<uint4*>(p.kv.K + to[j] + c) = k[j];
+          *reinterpret_cast<uint4*>(p.kv.V + to[j] + c) = v[j];
+        }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (to[j] >= 0) {
-        *reinterpret_cast<uint4*>(p.kv.K + to[j]) = k[j];
-        *reinterpret_cast<uint4*>(p.kv.V + to[j]) = v[j];
-      }
-  }
 }
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -555,7 +566,7 @@ cudaError_t launch_kv_evict(const mf_kv_evict_desc& d, const KvEvictWs& ws, uint
               : cudaLaunchKernelEx(&cfg, k_evict_select<EV_THR, true>, p);
   if (e != cudaSuccess) return e;
 
-  const int chunks = (int)std::max<int64_t>(1, (ws.moves + MV_ROWS - 1) / MV_ROWS);
+  const int chunks = (int)std::max<int64_t>(1, (ws.moves + MV_CHUNK - 1) / MV_CHUNK);
   cudaLaunchConfig_t mv{};
   mv.gridDim = dim3((unsigned)((int64_t)jobs * chunks));
   mv.blockDim = dim3(MV_THR);
