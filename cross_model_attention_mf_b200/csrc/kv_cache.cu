@@ -22,6 +22,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "paged_kv.cuh"
 
@@ -537,22 +538,25 @@ cudaError_t launch_kv_evict(const mf_kv_evict_desc& d, const KvEvictWs& ws, uint
   p.lens_out = d.seq_lens_out;
   p.ws = ws;
   const int jobs = d.kv.nseq * d.kv.h_kv;
-  // CTAs of 256 threads share a row, EV_SLOTS of its slots each, as long as a cluster of them
-  // holds it; a longer row takes CTAs of 512
+  // A row takes one CTA, of 256 threads up to EV_SLOTS slots and of 512 up to 32 each where there
+  // are many rows, half as many where there are few; longer ones a cluster of CTAs of 256 threads,
+  // EV_SLOTS of its slots each, as long as a cluster of them holds it, then of 512.  16 x 8 rows of
+  // 16000: alone 18.4 us, clusters 20.5; 4 x 8 rows: 17.8 and 13.7; 16 x 8 of 8192: 13.0 and 15.9;
+  // 8 rows of 6000: 11.3 and 12.5
   const bool wide = d.kv.max_len > (int64_t)EV_CLUSTER * 32 * EV_THR;
-  const int64_t most = 32 * (wide ? EV_WIDE : EV_THR);
+  const bool alone = d.kv.max_len <= (jobs > 64 ? 32 : 16) * EV_WIDE;
   int C = 1;
-  while (C < EV_CLUSTER && (int64_t)C * EV_SLOTS < d.kv.max_len) C *= 2;
+  while (!alone && C < EV_CLUSTER && (int64_t)C * EV_SLOTS < d.kv.max_len) C *= 2;
+  const int thr = wide || (alone && d.kv.max_len > EV_SLOTS) ? EV_WIDE : EV_THR;
+  const int keys = (int)std::min<int64_t>(32 * thr, ((int64_t)d.kv.max_len + C - 1) / C);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = wide ? allow_smem<&k_evict_select<EV_WIDE, false>>(dev, 4 * 32 * EV_WIDE)
-                                 : allow_smem<&k_evict_select<EV_THR, false>>(dev, 4 * 32 * EV_THR);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3((unsigned)((int64_t)jobs * C));
-  cfg.blockDim = dim3(wide ? EV_WIDE : EV_THR);
-  cfg.dynamicSmemBytes = (4 * (size_t)std::min<int64_t>(most, ((int64_t)d.kv.max_len + C - 1) / C) + 15) & ~size_t(15);
+  cfg.blockDim = dim3(thr);
+  cfg.dynamicSmemBytes = (4 * (size_t)keys + 15) & ~size_t(15);
   cfg.stream = st;
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)C;
@@ -560,10 +564,16 @@ cudaError_t launch_kv_evict(const mf_kv_evict_desc& d, const KvEvictWs& ws, uint
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  // (a lone CTA holds EV_SLOTS keys at most, which need no raised limit)
-  e = wide ? cudaLaunchKernelEx(&cfg, k_evict_select<EV_WIDE, false>, p)
-      : C > 1 ? cudaLaunchKernelEx(&cfg, k_evict_select<EV_THR, false>, p)
-              : cudaLaunchKernelEx(&cfg, k_evict_select<EV_THR, true>, p);
+  auto launch = [&](auto kernel) {
+    constexpr auto K = decltype(kernel)::value;
+    e = allow_smem<K>(dev, 4 * 32 * EV_WIDE);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, K, p);
+  };
+  using std::integral_constant;
+  if (alone && thr == EV_WIDE) launch(integral_constant<void (*)(EvictParams), &k_evict_select<EV_WIDE, true>>{});
+  else if (alone) launch(integral_constant<void (*)(EvictParams), &k_evict_select<EV_THR, true>>{});
+  else if (wide) launch(integral_constant<void (*)(EvictParams), &k_evict_select<EV_WIDE, false>>{});
+  else launch(integral_constant<void (*)(EvictParams), &k_evict_select<EV_THR, false>>{});
   if (e != cudaSuccess) return e;
 
   const int chunks = (int)std::max<int64_t>(1, (ws.moves + MV_CHUNK - 1) / MV_CHUNK);
