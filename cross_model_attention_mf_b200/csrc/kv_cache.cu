@@ -100,9 +100,10 @@ __global__ void __launch_bounds__(AP_THR) k_append(const __grid_constant__ Appen
 constexpr int BINS = 2048;
 constexpr int EV_CLUSTER = 8;     // portable cluster size
 constexpr int EV_LOADS = 8;       // slots a thread loads at a time
-constexpr int EV_SLOTS = 4096;    // slots a CTA takes before the cluster grows
-constexpr int EV_THR = 256;       // threads of a CTA, or
-constexpr int EV_WIDE = 512;      // where a cluster of the smaller ones cannot hold the row
+constexpr int EV_THR = 256;       // threads of a CTA for rows of up to
+constexpr int EV_SHORT = 4096;    // slots, and
+constexpr int EV_WIDE = 512;      // threads for longer ones
+constexpr int EV_SLOTS = 4096;    // slots a CTA of a cluster is left with where SMs would be idle
 
 struct EvictParams {
   KvView kv;
@@ -153,8 +154,8 @@ __device__ __forceinline__ uint32_t lowest_bits(uint32_t m, uint32_t n) {
 // SOLO: one CTA has the row to itself.
 template <int THR, bool SOLO>
 __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_constant__ EvictParams p) {
-  constexpr int WARPS = THR / 32, TILE = THR * 32, OWN = BINS / THR;
-  static_assert(OWN % 4 == 0 && 32 % OWN == 0 && BINS == 64 * 32, "two levels of the walk");
+  constexpr int WARPS = THR / 32, TILE = THR * 32;
+  static_assert(BINS == 64 * 32, "two levels of the walk");
   extern __shared__ __align__(16) uint32_t s_key[];
   __shared__ __align__(16) uint32_t s_hist[2][BINS];
   __shared__ __align__(8) uint32_t s_coarse[2][64];
@@ -270,17 +271,14 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
       }
     }
     __syncthreads();
-    // sums of 32 neighbouring bins: thread t adds up OWN of them
-    {
-      uint32_t sum = 0;
-#pragma unroll
-      for (int i = 0; i < OWN; i += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(hist + tid * OWN + i);
-        sum += v.x + v.y + v.z + v.w;
-      }
-#pragma unroll
-      for (int o = 1; o < 32 / OWN; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
-      if (tid % (32 / OWN) == 0) s_coarse[buf][tid / (32 / OWN)] = sum;
+    // sums of 32 neighbouring bins
+    for (int i = tid; i < BINS / 4; i += THR) {
+      const uint4 v = reinterpret_cast<const uint4*>(hist)[i];
+      uint32_t sum = v.x + v.y + v.z + v.w;
+      sum += __shfl_xor_sync(~0u, sum, 1);
+      sum += __shfl_xor_sync(~0u, sum, 2);
+      sum += __shfl_xor_sync(~0u, sum, 4);
+      if (i % 8 == 0) s_coarse[buf][i / 8] = sum;
     }
     sync();
     // The cluster's histograms are walked from the top: by one warp, 64 sums, then 32 bins
@@ -538,20 +536,20 @@ cudaError_t launch_kv_evict(const mf_kv_evict_desc& d, const KvEvictWs& ws, uint
   p.lens_out = d.seq_lens_out;
   p.ws = ws;
   const int jobs = d.kv.nseq * d.kv.h_kv;
-  // A row takes one CTA, of 256 threads up to EV_SLOTS slots and of 512 up to 32 each where there
-  // are many rows, half as many where there are few; longer ones a cluster of CTAs of 256 threads,
-  // EV_SLOTS of its slots each, as long as a cluster of them holds it, then of 512.  16 x 8 rows of
-  // 16000: alone 18.4 us, clusters 20.5; 4 x 8 rows: 17.8 and 13.7; 16 x 8 of 8192: 13.0 and 15.9;
-  // 8 rows of 6000: 11.3 and 12.5
-  const bool wide = d.kv.max_len > (int64_t)EV_CLUSTER * 32 * EV_THR;
-  const bool alone = d.kv.max_len <= (jobs > 64 ? 32 : 16) * EV_WIDE;
-  int C = 1;
-  while (!alone && C < EV_CLUSTER && (int64_t)C * EV_SLOTS < d.kv.max_len) C *= 2;
-  const int thr = wide || (alone && d.kv.max_len > EV_SLOTS) ? EV_WIDE : EV_THR;
-  const int keys = (int)std::min<int64_t>(32 * thr, ((int64_t)d.kv.max_len + C - 1) / C);
-  int dev = 0;
+  int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  // CTAs of a row: as few as hold its keys, for a barrier of a cluster takes a microsecond; a row
+  // of more than 8192 slots takes more of them, down to EV_SLOTS slots each, while SMs would be
+  // idle otherwise.  16 x 8 rows of 16000: alone 18.4 us, four CTAs each 20.5; 4 x 8 of them: 17.8
+  // and 12.8; 8 rows of 6000: 11.3 and (two each) 12.1
+  const int thr = d.kv.max_len <= EV_SHORT ? EV_THR : EV_WIDE;
+  int C = 1;
+  while (C < EV_CLUSTER && ((int64_t)C * 32 * thr < d.kv.max_len ||
+                            (d.kv.max_len > 2 * EV_SLOTS && (int64_t)C * EV_SLOTS < d.kv.max_len &&
+                             2 * (int64_t)C * jobs <= sms))) C *= 2;
+  const int keys = (int)std::min<int64_t>(32 * thr, ((int64_t)d.kv.max_len + C - 1) / C);
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3((unsigned)((int64_t)jobs * C));
@@ -570,10 +568,9 @@ cudaError_t launch_kv_evict(const mf_kv_evict_desc& d, const KvEvictWs& ws, uint
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, K, p);
   };
   using std::integral_constant;
-  if (alone && thr == EV_WIDE) launch(integral_constant<void (*)(EvictParams), &k_evict_select<EV_WIDE, true>>{});
-  else if (alone) launch(integral_constant<void (*)(EvictParams), &k_evict_select<EV_THR, true>>{});
-  else if (wide) launch(integral_constant<void (*)(EvictParams), &k_evict_select<EV_WIDE, false>>{});
-  else launch(integral_constant<void (*)(EvictParams), &k_evict_select<EV_THR, false>>{});
+  if (C == 1 && thr == EV_WIDE) launch(integral_constant<void (*)(EvictParams), &k_evict_select<EV_WIDE, true>>{});
+  else if (C == 1) launch(integral_constant<void (*)(EvictParams), &k_evict_select<EV_THR, true>>{});
+  else launch(integral_constant<void (*)(EvictParams), &k_evict_select<EV_WIDE, false>>{});
   if (e != cudaSuccess) return e;
 
   const int chunks = (int)std::max<int64_t>(1, (ws.moves + MV_CHUNK - 1) / MV_CHUNK);

@@ -314,6 +314,10 @@ EVICT = [
     ((40000,), 128, 0, 0, 1, 8, 32, BF),
     ((70, 70), 70, 10, 60, 2, 64, 1, F32),
     ((90,), 20, 10, 10, 1, 64, 16, BF),
+    # rows that a CTA of 512 threads takes whole (many of them), and that a cluster of them shares
+    ((16384, 15000), 300, 4, 20, 33, 8, 256, BF),
+    ((20000, 16385), 12000, 4, 64, 33, 8, 64, BF),
+    ((70001,), 20000, 4, 64, 2, 64, 64, F32),
 ]
 
 
