@@ -392,8 +392,9 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
     const int j0 = t0 + g0;
     const int at_h = j0 + 32 * lane - (int)kb, at_m = max(0, (int)(kb - kept_l));
     const bool clear = !copy_s || !copy_p;  // the first pass did it otherwise
+    const uint32_t some = __ballot_sync(~0u, (holes | movers | (clear ? gone : 0u)) != 0);
 #pragma unroll 4
-    for (int q = 0; q < groups; ++q) {
+    for (int q = some ? __ffs(some) - 1 : 0; q < 32 - __clz(some); ++q) {
       const uint32_t mh = __shfl_sync(~0u, holes, q), mm = __shfl_sync(~0u, movers, q);
       const int ah = __shfl_sync(~0u, at_h, q), am = __shfl_sync(~0u, at_m, q);
       const int j = j0 + 32 * q + lane;
