@@ -337,12 +337,6 @@ struct CoreF32 {
                              float* sl, int warp, int lane) {
     const KvView& kv = p.kv;
     const int nch = p.d >> 2;
-    __syncthreads();  // the previous unit's reads of sq are done
-    for (int i = threadIdx.x; i < HT * DP; i += NTHR) {
-      const int h = i / DP, c = i % DP;
-      sq[i] = h < u.nh && c < p.d ? reinterpret_cast<const float*>(p.Q + (int64_t)u.s * p.q_bytes)[(int64_t)(u.h0 + h) * p.d + c] : 0.0f;
-    }
-    __syncthreads();
     float4 o[HT][NV];
     float m[HT], l[HT];
 #pragma unroll
@@ -388,6 +382,12 @@ struct CoreF32 {
       cp_commit();
     }
     int64_t next = held(STAGES - 1) ? kv_offset(kv, id[STAGES - 1], at[STAGES - 1]) : -1;
+    // (the previous unit's reads of sq lie before the caller's barrier)
+    for (int i = threadIdx.x; i < HT * DP; i += NTHR) {
+      const int h = i / DP, c = i % DP;
+      sq[i] = h < u.nh && c < p.d ? reinterpret_cast<const float*>(p.Q + (int64_t)u.s * p.q_bytes)[(int64_t)(u.h0 + h) * p.d + c] : 0.0f;
+    }
+    __syncthreads();
     int stage = 0, fill = STAGES - 1;
     float* S = p.S ? p.S + ((int64_t)u.s * p.h_kv + u.hk) * kv.max_len * p.GP : nullptr;
     const int hg = u.h0 - u.hk * p.G;
