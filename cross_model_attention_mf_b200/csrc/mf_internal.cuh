@@ -108,6 +108,7 @@ cudaError_t launch_calib_solve(const double* gram, int h_s, int h_r, double ridg
 // single-token attention over the paged cache: scratch carved out of the caller's workspace
 struct PagedDecodeWs {
   int32_t* pre;     // [nseq + 1] tiles before each sequence
+  int64_t* per;     // tiles of a CTA
   float* lse2;      // [nseq][h_r]
   float* part_O;    // parts of the units cut between CTAs
   float2* part_ml;

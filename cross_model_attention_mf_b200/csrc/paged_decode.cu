@@ -31,6 +31,7 @@ constexpr int WARPS = 4;
 constexpr int NTHR = 32 * WARPS;
 constexpr int MAX_GRID = 512;     // CTAs of the main kernel (two partial results each)
 constexpr int MIN_TILES = WARPS;  // tiles a CTA takes at least: one per warp
+constexpr int ALIGN = WARPS;      // ALIGN, 2 ALIGN or 4 ALIGN tiles to a CTA where units have their own
 constexpr int MAX_SEQS = 4096;    // as the entry point checks
 constexpr int JOIN_THR = 256;
 constexpr int JOIN_KEYS = 2048;   // keys whose weights a CTA of the join kernel adds up
@@ -51,6 +52,7 @@ struct DecodeParams {
   float* score_out;    // or null
   int64_t score_stride;
   int32_t* pre;        // [nseq + 1] tiles before each sequence
+  int64_t* per;        // tiles of a CTA
   float* lse2;         // [nseq][h_r] of the units finished by one CTA
   float* part_O;       // [2 grid][HT][d]
   float2* part_ml;     // [2 grid][HT]
@@ -127,11 +129,10 @@ struct CoreBf16 {
   static constexpr int STAGES = DP == 64 ? 6 : DP == 128 ? 3 : DP == 192 ? 2 : 3;
   static constexpr int CTAS = DP == 256 ? 1 : 2;
   static constexpr int LDB = DP + 4;                 // conflict-free writes of the fragments
-  static constexpr int Q_FLOATS = 0;
   static_assert(HT * LDB * 4 <= STAGES * TILE, "O fits the warp's ring");
 
-  __device__ static void run(const DecodeParams& p, const Unit& u, uint8_t* ring, float*, float* sm,
-                             float* sl, int warp, int lane) {
+  __device__ static void run(const DecodeParams& p, const Unit& u, uint8_t* ring, float* sm, float* sl, int warp,
+                             int lane) {
     const KvView& kv = p.kv;
     const int g = lane >> 2, t = lane & 3;
     const int nch = p.d >> 3;
@@ -321,6 +322,10 @@ struct CoreBf16 {
   }
 };
 
+// A lane owns the same dims of Q, K, V and O (DIMS at a time), so that rows are read as they lie
+// and Q stays in registers; a lane's share of 4 heads x 8 keys is added up over the warp by
+// exchanges that halve the number of values, until lane (head r = lane / 8, key = lane % 8) holds
+// one score.  Reading Q from shared memory for every tile took three times as long.
 template <int DP_>
 struct CoreF32 {
   static constexpr int DP = DP_, TK = 8, HT = 8, ESZ = 4;
@@ -329,23 +334,33 @@ struct CoreF32 {
   static constexpr int STAGES = DP == 64 ? 6 : DP == 128 ? 3 : DP == 192 ? 2 : 3;
   static constexpr int CTAS = DP == 256 ? 1 : 2;
   static constexpr int LDB = DP;
-  static constexpr int Q_FLOATS = HT * DP;
-  static constexpr int NV = (CPR + 31) / 32;         // 16-byte chunks of a row per lane
+  static constexpr int DIMS = DP == 64 ? 2 : 4;      // neighbouring dims of a lane
+  static constexpr int NV = (DP / DIMS + 31) / 32;   // such groups of dims per lane
   static_assert(HT * LDB * 4 <= STAGES * TILE, "O fits the warp's ring");
 
-  __device__ static void run(const DecodeParams& p, const Unit& u, uint8_t* ring, float* sq, float* sm,
-                             float* sl, int warp, int lane) {
+  struct Vec {
+    float v[DIMS];
+  };
+  __device__ static bool in_row(int lane, int i) { return DIMS * (lane + 32 * i) < DP; }
+  __device__ static Vec load(const float* row, int lane, int i) {
+    Vec r;
+    if (!in_row(lane, i)) {
+#pragma unroll
+      for (int c = 0; c < DIMS; ++c) r.v[c] = 0.0f;
+    } else if (DIMS == 4) {
+      const float4 t = reinterpret_cast<const float4*>(row)[lane + 32 * i];
+      r.v[0] = t.x, r.v[1] = t.y, r.v[DIMS - 2] = t.z, r.v[DIMS - 1] = t.w;
+    } else {
+      const float2 t = reinterpret_cast<const float2*>(row)[lane + 32 * i];
+      r.v[0] = t.x, r.v[1] = t.y;
+    }
+    return r;
+  }
+
+  __device__ static void run(const DecodeParams& p, const Unit& u, uint8_t* ring, float* sm, float* sl, int warp,
+                             int lane) {
     const KvView& kv = p.kv;
     const int nch = p.d >> 2;
-    float4 o[HT][NV];
-    float m[HT], l[HT];
-#pragma unroll
-    for (int h = 0; h < HT; ++h) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) o[h][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      m[h] = -INFINITY;
-      l[h] = 0.0f;
-    }
     const int first = u.t0 + warp;
     const int n_my = first < u.t1 ? (u.t1 - first + WARPS - 1) / WARPS : 0;
     const uint32_t sring = smem_u32(ring);
@@ -363,7 +378,7 @@ struct CoreF32 {
         const int64_t ro = __shfl_sync(~0u, off, row);
         const bool ok = ro >= 0 && c < nch;
         const int64_t a = ok ? ro + hoff + c * 16 : 0;
-        const uint32_t dst = base + (row * CPR + (c ^ row)) * 16;
+        const uint32_t dst = base + idx * 16;
         cp16(dst, kv.K + a, ok ? 16u : 0u, policy);
         cp16(dst + TK * DP * ESZ, kv.V + a, ok ? 16u : 0u, policy);
       }
@@ -382,119 +397,179 @@ struct CoreF32 {
       cp_commit();
     }
     int64_t next = held(STAGES - 1) ? kv_offset(kv, id[STAGES - 1], at[STAGES - 1]) : -1;
-    // (the previous unit's reads of sq lie before the caller's barrier)
-    for (int i = threadIdx.x; i < HT * DP; i += NTHR) {
-      const int h = i / DP, c = i % DP;
-      sq[i] = h < u.nh && c < p.d ? reinterpret_cast<const float*>(p.Q + (int64_t)u.s * p.q_bytes)[(int64_t)(u.h0 + h) * p.d + c] : 0.0f;
-    }
-    __syncthreads();
+    Vec q[HT][NV], o[HT][NV];
+#pragma unroll
+    for (int h = 0; h < HT; ++h)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < DIMS; ++c) {
+          const int dim = DIMS * (lane + 32 * i) + c;
+          o[h][i].v[c] = 0.0f;
+          q[h][i].v[c] = h < u.nh && dim < p.d
+              ? reinterpret_cast<const float*>(p.Q + (int64_t)u.s * p.q_bytes)[(int64_t)(u.h0 + h) * p.d + dim] : 0.0f;
+        }
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // of head 4 b + r; l over the lane's keys
     int stage = 0, fill = STAGES - 1;
     float* S = p.S ? p.S + ((int64_t)u.s * p.h_kv + u.hk) * kv.max_len * p.GP : nullptr;
     const int hg = u.h0 - u.hk * p.G;
-    const int kl = lane & 7, part = lane >> 3;
+    const int kl = lane & 7, r = lane >> 3;
     for (int k = 0; k < n_my; ++k) {
       cp_wait<STAGES - 2>();
       __syncwarp();
       if (k + STAGES - 1 < n_my) issue(fill, next);
       cp_commit();
       next = rows_of(k + STAGES);
-      const float4* Kt = reinterpret_cast<const float4*>(ring + stage * TILE);
-      const float4* Vt = Kt + TK * CPR;
+      const float* Kt = reinterpret_cast<const float*>(ring + stage * TILE);
+      const float* Vt = Kt + TK * DP;
       if (++stage == STAGES) stage = 0;
       if (++fill == STAGES) fill = 0;
-      // lane (key kl, part): every fourth 16-byte chunk of the key's row, all heads
-      float x[HT];
-#pragma unroll
-      for (int h = 0; h < HT; ++h) x[h] = 0.0f;
-#pragma unroll 4
-      for (int c = part; c < CPR; c += 4) {
-        const float4 kk = Kt[kl * CPR + (c ^ kl)];
-#pragma unroll
-        for (int h = 0; h < HT; ++h) {
-          const float4 qq = reinterpret_cast<const float4*>(sq)[h * CPR + c];
-          x[h] = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, fmaf(kk.w, qq.w, x[h]))));
-        }
-      }
       const int key = (first + k * WARPS) * TK + kl;
       const bool in = key < u.len;
+      float w[2] = {0.0f, 0.0f}, al[2] = {1.0f, 1.0f};
+      bool moved = false;
 #pragma unroll
-      for (int h = 0; h < HT; ++h) {
-        float v = x[h];
-        v += __shfl_xor_sync(~0u, v, 8);
-        v += __shfl_xor_sync(~0u, v, 16);
-        v = in ? v * p.c2 : -INFINITY;
-        if (S && in && part == 0 && h < u.nh) S[(int64_t)key * p.GP + hg + h] = v;
+      for (int b = 0; b < 2; ++b) {
+        if (4 * b >= u.nh) break;  // the same in the whole warp
+        float x[4][8];
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[h][j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const Vec t = load(Kt + j * DP, lane, i);
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+              for (int c = 0; c < DIMS; ++c) x[h][j] = fmaf(t.v[c], q[4 * b + h][i].v[c], x[h][j]);
+          }
+        // keys over lane bits 2, 1, 0
+#pragma unroll
+        for (int n = 4; n; n >>= 1)
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int j = 0; j < n; ++j) {
+              const bool up = lane & n;
+              const float give = up ? x[h][j] : x[h][j + n], keep = up ? x[h][j + n] : x[h][j];
+              x[h][j] = keep + __shfl_xor_sync(~0u, give, n);
+            }
+        // heads over lane bits 4, 3
+#pragma unroll
+        for (int n = 2; n; n >>= 1)
+#pragma unroll
+          for (int h = 0; h < n; ++h) {
+            const bool up = lane & (8 * n);
+            const float give = up ? x[h][0] : x[h + n][0], keep = up ? x[h + n][0] : x[h][0];
+            x[h][0] = keep + __shfl_xor_sync(~0u, give, 8 * n);
+          }
+        const float v = in ? x[0][0] * p.c2 : -INFINITY;
+        if (S && in && 4 * b + r < u.nh) S[(int64_t)key * p.GP + hg + 4 * b + r] = v;
         float mx = v;
         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
-        const float mn = fmaxf(m[h], mx);
+        const float mn = fmaxf(m[b], mx);
         const float mu = mn == -INFINITY ? 0.0f : mn;
-        const float al = ex2(m[h] - mu);
-        m[h] = mn;
-        x[h] = ex2(v - mu);
-        l[h] = l[h] * al + x[h];
+        al[b] = ex2(m[b] - mu);
+        moved |= mn != m[b];
+        m[b] = mn;
+        w[b] = ex2(v - mu);
+        l[b] = l[b] * al[b] + w[b];
+      }
+      if (__any_sync(~0u, moved)) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          o[h][i].x *= al;
-          o[h][i].y *= al;
-          o[h][i].z *= al;
-          o[h][i].w *= al;
+        for (int h = 0; h < HT; ++h) {
+          const float f = __shfl_sync(~0u, al[h >> 2], 8 * (h & 3));
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int c = 0; c < DIMS; ++c) o[h][i].v[c] *= f;
         }
       }
 #pragma unroll
       for (int j = 0; j < TK; ++j) {
-        float4 v[NV];
+        Vec t[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = lane + 32 * i;
-          v[i] = c < CPR ? Vt[j * CPR + (c ^ j)] : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+        for (int i = 0; i < NV; ++i) t[i] = load(Vt + j * DP, lane, i);
 #pragma unroll
-        for (int h = 0; h < HT; ++h) {
-          const float w = __shfl_sync(~0u, x[h], j);
+        for (int b = 0; b < 2; ++b) {
+          if (4 * b >= u.nh) break;
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            o[h][i].x = fmaf(w, v[i].x, o[h][i].x);
-            o[h][i].y = fmaf(w, v[i].y, o[h][i].y);
-            o[h][i].z = fmaf(w, v[i].z, o[h][i].z);
-            o[h][i].w = fmaf(w, v[i].w, o[h][i].w);
+          for (int h = 4 * b; h < 4 * b + 4; ++h) {
+            const float f = __shfl_sync(~0u, w[b], 8 * (h & 3) + j);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+              for (int c = 0; c < DIMS; ++c) o[h][i].v[c] = fmaf(f, t[i].v[c], o[h][i].v[c]);
           }
         }
       }
     }
     cp_wait<0>();
     __syncwarp();
-    float4* buf = reinterpret_cast<float4*>(ring);
+    float* buf = reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int h = 0; h < HT; ++h) {
-      float v = l[h];
+    for (int b = 0; b < 2; ++b) {
+      float v = l[b];
       v += __shfl_xor_sync(~0u, v, 1);
       v += __shfl_xor_sync(~0u, v, 2);
       v += __shfl_xor_sync(~0u, v, 4);
-      if (lane == 0) {
-        sm[h] = m[h];
-        sl[h] = v;
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = lane + 32 * i;
-        if (c < CPR) buf[h * (LDB / 4) + c] = o[h][i];
+      if (kl == 0) {
+        sm[4 * b + r] = m[b];
+        sl[4 * b + r] = v;
       }
     }
+#pragma unroll
+    for (int h = 0; h < HT; ++h)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (in_row(lane, i))
+#pragma unroll
+          for (int c = 0; c < DIMS; ++c) buf[h * LDB + DIMS * (lane + 32 * i) + c] = o[h][i].v[c];
   }
 };
 
-// tiles before each sequence, in shared memory; a sequence of length 0 takes one (empty) tile, so
-// that its outputs are written like any other's
-__device__ inline void scan_tiles(const KvView& kv, int tk, int32_t* pre, bool report) {
+__device__ __forceinline__ int tiles_of(int len, int tk) { return max(1, (len + tk - 1) / tk); }
+__device__ __forceinline__ int round_up(int n, int to) { return (n + to - 1) / to * to; }
+
+// Tiles before each sequence on the line that the CTAs share (`pre`, shared memory), and the tiles
+// of a CTA, which are returned.  A sequence of length 0 takes one (empty) tile, so that its outputs
+// are written like any other's.  If every unit can have CTAs of its own, ALIGN << k tiles each, its
+// stretch of the line is rounded up to them: no CTA then starts over with a second unit, which
+// takes 2 us of the 11 that a small call lasts.
+__device__ inline int64_t scan_tiles(const DecodeParams& p, int tk, int32_t* pre, bool report) {
   __shared__ int s_w[WARPS];
-  int base = 0;
+  __shared__ int s_n[3];
+  const KvView& kv = p.kv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x < 3) s_n[threadIdx.x] = 0;
+  __syncthreads();
+  int c[3] = {0, 0, 0};
+  for (int s = threadIdx.x; s < kv.nseq; s += NTHR) {
+    const int n = tiles_of(kv_len(kv, s, report), tk);
+    pre[s] = n;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) c[k] += min((n + (ALIGN << k) - 1) / (ALIGN << k), MAX_GRID + 1);
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    c[k] = __reduce_add_sync(~0u, c[k]);
+    if (lane == 0) atomicAdd(&s_n[k], c[k]);
+  }
+  __syncthreads();
+  int align = 0;
+#pragma unroll
+  for (int k = 2; k >= 0; --k)
+    if (s_n[k] <= p.grid / p.U) align = ALIGN << k;
+  int base = 0;
   for (int s0 = 0; s0 < kv.nseq; s0 += NTHR) {
     const int s = s0 + threadIdx.x;
-    int n = 0;
-    if (s < kv.nseq) n = max(1, (kv_len(kv, s, report) + tk - 1) / tk);
+    int n = s < kv.nseq ? pre[s] : 0;
+    if (align) n = round_up(n, align);
     int x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -515,11 +590,7 @@ __device__ inline void scan_tiles(const KvView& kv, int tk, int32_t* pre, bool r
   }
   if (threadIdx.x == 0) pre[kv.nseq] = base;
   __syncthreads();
-}
-
-__device__ __forceinline__ int64_t tiles_per_cta(int64_t total, int grid) {
-  const int64_t per = div_floor(total + grid - 1, grid);
-  return per < MIN_TILES ? MIN_TILES : per;
+  return align ? align : max((int64_t)MIN_TILES, div_floor((int64_t)base * p.U + p.grid - 1, p.grid));
 }
 
 template <class Core>
@@ -529,8 +600,7 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
   constexpr int RING = Core::STAGES * Core::TILE;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem + warp * RING;
-  float* sq = reinterpret_cast<float*>(smem + WARPS * RING);
-  int32_t* pre = reinterpret_cast<int32_t*>(sq + Core::Q_FLOATS);
+  int32_t* pre = reinterpret_cast<int32_t*>(smem + WARPS * RING);
 
   // the join kernel may take its place now; it waits for this grid before its first access
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -542,11 +612,12 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
     end = x + 1;
     s = (int)(x / p.U);
   } else {
-    scan_tiles(p.kv, Core::TK, pre, blockIdx.x == 0);
-    if (blockIdx.x == 0)
+    const int64_t per = scan_tiles(p, Core::TK, pre, blockIdx.x == 0);
+    if (blockIdx.x == 0) {
       for (int i = threadIdx.x; i <= p.kv.nseq; i += NTHR) p.pre[i] = pre[i];
+      if (threadIdx.x == 0) *p.per = per;
+    }
     const int64_t total = (int64_t)pre[p.kv.nseq] * p.U;
-    const int64_t per = tiles_per_cta(total, p.grid);
     x = per * blockIdx.x;
     end = min(total, x + per);
     int hi = p.kv.nseq;  // the sequence whose stretch holds x
@@ -564,7 +635,7 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
     if (p.whole) {
       ui = (int)(x - (int64_t)s * p.U);
       u.t0 = 0;
-      u.t1 = max(1, (u.len + Core::TK - 1) / Core::TK);
+      u.t1 = tiles_of(u.len, Core::TK);
       begins = whole = true;
       ++x;
     } else {
@@ -572,18 +643,19 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
       const int64_t rel = x - (int64_t)pre[s] * p.U;
       ui = (int)div_floor(rel, nt);
       u.t0 = (int)(rel - (int64_t)ui * nt);
-      u.t1 = (int)min((int64_t)nt, u.t0 + (end - x));
+      const int to = (int)min((int64_t)nt, u.t0 + (end - x));
+      u.t1 = min(to, tiles_of(u.len, Core::TK));  // past it the stretch is rounded up
       begins = u.t0 == 0;
-      whole = begins && u.t1 == nt;
-      x += u.t1 - u.t0;
-      if (ui == p.U - 1 && u.t1 == nt) ++s;
+      whole = begins && to == nt;
+      x += to - u.t0;
+      if (ui == p.U - 1 && to == nt) ++s;
     }
     u.hk = ui / p.hb;
     const int in_group = (ui - u.hk * p.hb) * Core::HT;
     u.h0 = u.hk * p.G + in_group;
     u.nh = min(Core::HT, p.G - in_group);
 
-    Core::run(p, u, ring, sq, s_m[warp], s_l[warp], warp, lane);
+    Core::run(p, u, ring, s_m[warp], s_l[warp], warp, lane);
     __syncthreads();
     // join the warps; a finished unit writes O, a cut one its part
     const int half = p.d >> 1;
@@ -632,8 +704,8 @@ struct Parts {
 
 __device__ __forceinline__ Parts unit_parts(const DecodeParams& p, int s, int ui) {
   if (p.whole) return {0, 1};
-  const int all = p.pre[p.kv.nseq], before = p.pre[s], nt = p.pre[s + 1] - before;
-  const int64_t per = tiles_per_cta((int64_t)all * p.U, p.grid);
+  const int before = p.pre[s], nt = p.pre[s + 1] - before;
+  const int64_t per = *p.per;
   const int64_t at = (int64_t)before * p.U + (int64_t)ui * nt;
   const int64_t c0 = div_floor(at, per);
   return {c0, (int)(div_floor(at + nt - 1, per) - c0) + 1};
@@ -829,12 +901,14 @@ size_t paged_decode_ws(const mf_paged_decode_desc& d, PagedDecodeWs* ws, void* b
     return q;
   };
   char* pre = take(4 * ((size_t)d.kv.nseq + 1));
+  char* per = take(sizeof(int64_t));
   char* lse2 = take(4 * (size_t)d.kv.nseq * d.h_r);
   char* po = take(sizeof(float) * 2 * MAX_GRID * (size_t)HT * d.kv.d);
   char* ml = take(sizeof(float2) * 2 * MAX_GRID * (size_t)HT);
   char* S = d.score_out ? take(4 * (size_t)d.kv.nseq * d.kv.h_kv * d.kv.max_len * GP) : nullptr;
   if (ws) {
     ws->pre = reinterpret_cast<int32_t*>(pre);
+    ws->per = reinterpret_cast<int64_t*>(per);
     ws->lse2 = reinterpret_cast<float*>(lse2);
     ws->part_O = reinterpret_cast<float*>(po);
     ws->part_ml = reinterpret_cast<float2*>(ml);
@@ -868,6 +942,7 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   p.score_out = d.score_out;
   p.score_stride = d.score_stride;
   p.pre = ws.pre;
+  p.per = ws.per;
   p.lse2 = ws.lse2;
   p.part_O = ws.part_O;
   p.part_ml = ws.part_ml;
@@ -881,10 +956,9 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   cudaError_t err = cudaSuccess;
   auto launch = [&](auto core) {
     using Core = decltype(core);
-    const size_t smem = (size_t)WARPS * Core::STAGES * Core::TILE + 4 * (size_t)Core::Q_FLOATS +
-                        (p.whole ? 0 : 4 * ((size_t)p.kv.nseq + 1));
+    const size_t smem = (size_t)WARPS * Core::STAGES * Core::TILE + (p.whole ? 0 : 4 * ((size_t)p.kv.nseq + 1));
     // room for the scan of the largest batch
-    err = allow_smem<&k_decode<Core>>(dev, WARPS * Core::STAGES * Core::TILE + 4 * Core::Q_FLOATS + 4 * (MAX_SEQS + 1));
+    err = allow_smem<&k_decode<Core>>(dev, WARPS * Core::STAGES * Core::TILE + 4 * (MAX_SEQS + 1));
     if (err != cudaSuccess) return;
     p.grid = p.whole ? p.kv.nseq * p.U : std::min(MAX_GRID, sms * Core::CTAS);
     k_decode<Core><<<p.grid, NTHR, smem, st>>>(p);
