@@ -58,6 +58,7 @@ struct DecodeParams {
   float2* part_ml;     // [2 grid][HT]
   int grid;
   int whole;           // every unit is finished by one CTA
+  int own_scores;      // and its group has no other unit: the CTA adds up the weights too
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -593,10 +594,68 @@ __device__ inline int64_t scan_tiles(const DecodeParams& p, int tk, int32_t* pre
   return align ? align : max((int64_t)MIN_TILES, div_floor((int64_t)base * p.U + p.grid - 1, p.grid));
 }
 
+// sum of 2^(x - lse2) over the first n of V heads (the others are padding); an empty row, of x = -inf
+// and any lse2, adds 0
+template <int V>
+__device__ __forceinline__ float weights(const float (&x)[V], const float* lse2, int n) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < n) sum += ex2(x[i] - lse2[i]);
+  return sum;
+}
+template <int V> __device__ __forceinline__ void load_x(const float* x, float (&v)[V]) {
+  if (V == 4) {
+    const float4 t = __ldcs(reinterpret_cast<const float4*>(x));
+    v[0] = t.x, v[1] = t.y, v[V - 2] = t.z, v[V - 1] = t.w;
+  } else {
+    const float2 t = __ldcs(reinterpret_cast<const float2*>(x));
+    v[0] = t.x, v[1] = t.y;
+  }
+}
+
+// Keys j0 .. j1 of one row: the group's weights, V heads to a load.  A thread's first loads go out
+// before `ready` has found lse2 (shared memory).
+template <int V, int THR, class Ready>
+__device__ __forceinline__ void add_weights(const DecodeParams& p, int64_t row, int j0, int j1, const float* lse2,
+                                            Ready ready) {
+  constexpr int UN = 4;
+  for (int j = j0 + threadIdx.x; j < j1 || j - j0 < THR; j += UN * THR) {
+    const float* S = p.S + (row * p.kv.max_len + j) * p.GP;
+    const float* in = p.score_in ? p.score_in + row * p.score_stride + j : nullptr;
+    float* out = p.score_out + row * p.score_stride + j;
+    const int rem = j1 - j;
+    float old[UN], x[UN][V];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      old[i] = 0.0f;
+      if (i * THR < rem) {
+        if (in) old[i] = in[i * THR];
+        load_x<V>(S + i * THR * p.GP, x[i]);
+      }
+    }
+    if (j - j0 < THR) ready();
+    float sum[UN];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) sum[i] = i * THR < rem ? weights<V>(x[i], lse2, p.G) : 0.0f;
+    for (int h = V; h < p.GP; h += V) {
+#pragma unroll
+      for (int i = 0; i < UN; ++i)
+        if (i * THR < rem) load_x<V>(S + i * THR * p.GP + h, x[i]);
+#pragma unroll
+      for (int i = 0; i < UN; ++i)
+        if (i * THR < rem) sum[i] += weights<V>(x[i], lse2 + h, p.G - h);
+    }
+#pragma unroll
+    for (int i = 0; i < UN; ++i)
+      if (i * THR < rem) out[i * THR] = old[i] + sum[i];
+  }
+}
+
 template <class Core>
 __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_constant__ DecodeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[WARPS][Core::HT], s_l[WARPS][Core::HT];
+  __shared__ float s_m[WARPS][Core::HT], s_l[WARPS][Core::HT], s_lse2[Core::HT];
   constexpr int RING = Core::STAGES * Core::TILE;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem + warp * RING;
@@ -682,8 +741,9 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
         if (c == 0) {
           const float v = L == 0.0f ? -INFINITY : mu + log2f(L);
           const int64_t r = (int64_t)u.s * p.h_r + u.h0 + h;
-          if (p.lse2) p.lse2[r] = v;
+          p.lse2[r] = v;
           if (p.lse) p.lse[r] = v * LN2;
+          s_lse2[h] = v == -INFINITY ? 0.0f : v;
         }
       } else {
         const int64_t slot = 2 * (int64_t)blockIdx.x + (begins ? 1 : 0);
@@ -692,6 +752,12 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
       }
     }
     __syncthreads();
+  }
+  if (p.own_scores) {  // the CTA had a whole group: it turns the x_j that it stored into weights itself
+    const int row = blockIdx.x, len = kv_len(p.kv, row / p.h_kv, false);  // one unit to a key head
+    auto ready = [] {};
+    if (p.GP % 4 == 0) add_weights<4, NTHR>(p, row, 0, len, s_lse2, ready);
+    else add_weights<2, NTHR>(p, row, 0, len, s_lse2, ready);
   }
 }
 
@@ -726,64 +792,6 @@ __device__ __forceinline__ float2 join_stats(const DecodeParams& p, const Parts&
 #pragma unroll
   for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(~0u, L, o);
   return make_float2(mu, L);
-}
-
-// sum of 2^(x - lse2) over the first n of V heads (the others are padding); an empty row, of x = -inf
-// and any lse2, adds 0
-template <int V>
-__device__ __forceinline__ float weights(const float (&x)[V], const float* lse2, int n) {
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (i < n) sum += ex2(x[i] - lse2[i]);
-  return sum;
-}
-template <int V> __device__ __forceinline__ void load_x(const float* x, float (&v)[V]) {
-  if (V == 4) {
-    const float4 t = __ldcs(reinterpret_cast<const float4*>(x));
-    v[0] = t.x, v[1] = t.y, v[V - 2] = t.z, v[V - 1] = t.w;
-  } else {
-    const float2 t = __ldcs(reinterpret_cast<const float2*>(x));
-    v[0] = t.x, v[1] = t.y;
-  }
-}
-
-// Keys j0 .. j1 of one row: the group's weights, V heads to a load.  A thread's first loads go out
-// before `ready` has found lse2 (shared memory).
-template <int V, class Ready>
-__device__ __forceinline__ void add_weights(const DecodeParams& p, int64_t row, int j0, int j1, const float* lse2,
-                                            Ready ready) {
-  constexpr int UN = 4;
-  for (int j = j0 + threadIdx.x; j < j1 || j - j0 < JOIN_THR; j += UN * JOIN_THR) {
-    const float* S = p.S + (row * p.kv.max_len + j) * p.GP;
-    const float* in = p.score_in ? p.score_in + row * p.score_stride + j : nullptr;
-    float* out = p.score_out + row * p.score_stride + j;
-    const int rem = j1 - j;
-    float old[UN], x[UN][V];
-#pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      old[i] = 0.0f;
-      if (i * JOIN_THR < rem) {
-        if (in) old[i] = in[i * JOIN_THR];
-        load_x<V>(S + i * JOIN_THR * p.GP, x[i]);
-      }
-    }
-    if (j - j0 < JOIN_THR) ready();
-    float sum[UN];
-#pragma unroll
-    for (int i = 0; i < UN; ++i) sum[i] = i * JOIN_THR < rem ? weights<V>(x[i], lse2, p.G) : 0.0f;
-    for (int h = V; h < p.GP; h += V) {
-#pragma unroll
-      for (int i = 0; i < UN; ++i)
-        if (i * JOIN_THR < rem) load_x<V>(S + i * JOIN_THR * p.GP + h, x[i]);
-#pragma unroll
-      for (int i = 0; i < UN; ++i)
-        if (i * JOIN_THR < rem) sum[i] += weights<V>(x[i], lse2 + h, p.G - h);
-    }
-#pragma unroll
-    for (int i = 0; i < UN; ++i)
-      if (i * JOIN_THR < rem) out[i * JOIN_THR] = old[i] + sum[i];
-  }
 }
 
 // a += the parts first, first + step, .. of four columns of head h; part k is scaled to the row's m
@@ -875,8 +883,8 @@ __global__ void __launch_bounds__(JOIN_THR, 4) k_decode_join(const __grid_consta
     __syncthreads();
   };
   const int j1 = (int)min((int64_t)len, j0 + JOIN_KEYS);
-  if (p.GP % 4 == 0) add_weights<4>(p, sg, (int)j0, j1, s_lse2, ready);
-  else add_weights<2>(p, sg, (int)j0, j1, s_lse2, ready);
+  if (p.GP % 4 == 0) add_weights<4, JOIN_THR>(p, sg, (int)j0, j1, s_lse2, ready);
+  else add_weights<2, JOIN_THR>(p, sg, (int)j0, j1, s_lse2, ready);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -886,9 +894,11 @@ int head_tile(const mf_paged_decode_desc& d) {
   return d.kv.dtype == MF_BF16 && d.h_r / d.kv.h_kv > 8 ? 16 : 8;
 }
 
-// One CTA per unit, without a second launch, for lengths up to this many keys: splitting them
-// would leave a warp one or two tiles.
-constexpr int WHOLE_KEYS = 256;
+// One CTA per unit, without a second launch, for lengths up to this many keys.  Where units do not
+// fill the GPU, splitting them takes 9 to 10 us at any length: bf16 keys take that long from 512 on
+// (8 tiles a warp), float32 keys from 128 on.  More units than CTAs gain from it a little longer:
+// 512 units of 200 float32 keys 24 us, split 29; of 500 keys 47 and 46.
+int whole_keys(const mf_paged_decode_desc& d, bool fill) { return d.kv.dtype == MF_BF16 ? 512 : fill ? 256 : 128; }
 
 }  // namespace
 
@@ -946,7 +956,6 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   p.lse2 = ws.lse2;
   p.part_O = ws.part_O;
   p.part_ml = ws.part_ml;
-  p.whole = d.kv.max_len <= WHOLE_KEYS;
 
   int dev = 0, sms = 0;
   cudaError_t e0 = cudaGetDevice(&dev);
@@ -956,11 +965,14 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   cudaError_t err = cudaSuccess;
   auto launch = [&](auto core) {
     using Core = decltype(core);
+    const int resident = std::min(MAX_GRID, sms * Core::CTAS), units = p.kv.nseq * p.U;
+    p.whole = d.kv.max_len <= whole_keys(d, units > resident);
+    p.own_scores = p.whole && p.S && p.hb == 1;
+    p.grid = p.whole ? units : resident;
     const size_t smem = (size_t)WARPS * Core::STAGES * Core::TILE + (p.whole ? 0 : 4 * ((size_t)p.kv.nseq + 1));
     // room for the scan of the largest batch
     err = allow_smem<&k_decode<Core>>(dev, WARPS * Core::STAGES * Core::TILE + 4 * (MAX_SEQS + 1));
     if (err != cudaSuccess) return;
-    p.grid = p.whole ? p.kv.nseq * p.U : std::min(MAX_GRID, sms * Core::CTAS);
     k_decode<Core><<<p.grid, NTHR, smem, st>>>(p);
     err = cudaGetLastError();
   };
@@ -981,7 +993,7 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
     else if (D == 192) launch(CoreBf16<192, 2>{});
     else launch(CoreBf16<256, 2>{});
   }
-  if (err != cudaSuccess || (p.whole && !p.score_out)) return err;
+  if (err != cudaSuccess || (p.whole && (!p.score_out || p.own_scores))) return err;
 
   cudaLaunchConfig_t cfg{};
   // parts of a row if all were equally long: from 8 on its join is split over a CTA's warps
