@@ -6,13 +6,16 @@
 // 4 len h_r d operations on 2 len h_kv d elements, so HBM bandwidth bounds the call at any
 // group size the tensor cores serve.
 //
-// Split.  A unit is (sequence, key head, block of up to HT query heads of its group); the units
-// of the batch, cut into tiles of TK keys, lie one after another on a line that the CTAs share
-// evenly: whatever the lengths, every CTA gets the same number of tiles.  A CTA walks the units
-// of its stretch; a unit that lies wholly inside is finished there, a unit cut by a stretch's end
-// leaves (m, l, O) in the workspace, at most two per CTA, and k_decode_join adds the parts in
-// order.  Within a CTA the four warps take tiles in turn, each with its own ring of asynchronous
-// copies and its own (m, l, O): no CTA barrier inside a unit.
+// Split.  A unit is (sequence, key head, block of up to HT query heads of its group).  The units
+// of a sequence go in F bundles of P; the bundles of the batch, cut into tiles of TK keys, lie one
+// after another on a line that groups of P CTAs share evenly, each CTA with a unit of the bundle:
+// whatever the lengths, every CTA gets the same number of tiles, and the CTAs of a group walk
+// through the same slots together, whose rows are neighbours in memory.  (With every unit on a line
+// of its own, rows of 160 bytes cost 1.5 times their bytes in DRAM traffic.)  A CTA finishes a unit
+// that lies wholly inside its stretch; a unit cut by a stretch's end leaves (m, l, O) in the
+// workspace, at most two per CTA, and k_decode_join adds the parts in order.  Within a CTA the
+// four warps take tiles in turn, each with its own ring of asynchronous copies and its own
+// (m, l, O): no CTA barrier inside a unit.
 //
 // Gathered weights need the final lse, so the main kernel stores x_j (4 bytes per query head and
 // key, against 2 d elements per key head) and the join kernel turns them into weights.
@@ -56,7 +59,7 @@ struct DecodeParams {
   float* lse2;         // [nseq][h_r] of the units finished by one CTA
   float* part_O;       // [2 grid][HT][d]
   float2* part_ml;     // [2 grid][HT]
-  int grid;
+  int P, F, groups;    // units of a bundle, bundles of a sequence, groups of CTAs
   int whole;           // every unit is finished by one CTA
   int own_scores;      // and its group has no other unit: the CTA adds up the weights too
 };
@@ -126,8 +129,11 @@ template <int DP_, int NT>
 struct CoreBf16 {
   static constexpr int DP = DP_, TK = 16, HT = 8 * NT, ESZ = 2;
   static constexpr int CPR = DP / 8;                 // 16-byte chunks per row
-  static constexpr int TILE = 2 * TK * DP * ESZ;     // K rows, then V rows
+  static constexpr int HALF = TK * DP * ESZ;         // K rows, then V rows
+  static constexpr int TILE = 2 * HALF;
   static constexpr int STAGES = DP == 64 ? 6 : DP == 128 ? 3 : DP == 192 ? 2 : 3;
+  // eight rows' chunks of one column fall on different banks
+  __device__ static uint32_t place(int row, int c) { return (row * CPR + (c ^ (row & 7))) * 16; }
   static constexpr int CTAS = DP == 256 ? 1 : 2;
   static constexpr int LDB = DP + 4;                 // conflict-free writes of the fragments
   static_assert(HT * LDB * 4 <= STAGES * TILE, "O fits the warp's ring");
@@ -155,9 +161,9 @@ struct CoreBf16 {
         const int64_t ro = __shfl_sync(~0u, off, row);
         const bool ok = ro >= 0 && c < nch;
         const int64_t a = ok ? ro + hoff + c * 16 : 0;
-        const uint32_t dst = base + (row * CPR + (c ^ (row & 7))) * 16;
+        const uint32_t dst = base + place(row, c);
         cp16(dst, kv.K + a, ok ? 16u : 0u, policy);
-        cp16(dst + TK * DP * ESZ, kv.V + a, ok ? 16u : 0u, policy);
+        cp16(dst + HALF, kv.V + a, ok ? 16u : 0u, policy);
       }
     };
     // the first tiles' pages are looked up together
@@ -208,7 +214,7 @@ struct CoreBf16 {
       if (k + STAGES - 1 < n_my) issue(fill, next);
       cp_commit();
       next = rows_of(k + STAGES);
-      const uint32_t kb = sring + stage * TILE, vb = kb + TK * DP * ESZ;
+      const uint32_t kb = sring + stage * TILE, vb = kb + HALF;
       if (++stage == STAGES) stage = 0;
       if (++fill == STAGES) fill = 0;
 
@@ -223,7 +229,7 @@ struct CoreBf16 {
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks) {
           uint32_t a[4];
-          ldm4(a, kb + (row * CPR + ((2 * ks + hi) ^ (row & 7))) * 16);
+          ldm4(a, kb + place(row, 2 * ks + hi));
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma16816(sc[ks & 1][n], a, q[ks][n][0], q[ks][n][1]);
         }
@@ -289,7 +295,7 @@ struct CoreBf16 {
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i) {
           uint32_t a[4];
-          ldm4t(a, vb + (row * CPR + ((2 * i + hi) ^ (row & 7))) * 16);
+          ldm4t(a, vb + place(row, 2 * i + hi));
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             mma16816(o[i][n], a, phi[n][0], phi[n][1]);
@@ -537,8 +543,8 @@ struct CoreF32 {
 __device__ __forceinline__ int tiles_of(int len, int tk) { return max(1, (len + tk - 1) / tk); }
 __device__ __forceinline__ int round_up(int n, int to) { return (n + to - 1) / to * to; }
 
-// Tiles before each sequence on the line that the CTAs share (`pre`, shared memory), and the tiles
-// of a CTA, which are returned.  A sequence of length 0 takes one (empty) tile, so that its outputs
+// Tiles before each sequence on the line of one bundle (`pre`, shared memory), and the tiles of a
+// CTA, which are returned.  A sequence of length 0 takes one (empty) tile, so that its outputs
 // are written like any other's.  If every unit can have CTAs of its own, ALIGN << k tiles each, its
 // stretch of the line is rounded up to them: no CTA then starts over with a second unit, which
 // takes 2 us of the 11 that a small call lasts.
@@ -565,7 +571,7 @@ __device__ inline int64_t scan_tiles(const DecodeParams& p, int tk, int32_t* pre
   int align = 0;
 #pragma unroll
   for (int k = 2; k >= 0; --k)
-    if (s_n[k] <= p.grid / p.U) align = ALIGN << k;
+    if (s_n[k] <= p.groups / p.F) align = ALIGN << k;
   int base = 0;
   for (int s0 = 0; s0 < kv.nseq; s0 += NTHR) {
     const int s = s0 + threadIdx.x;
@@ -591,7 +597,7 @@ __device__ inline int64_t scan_tiles(const DecodeParams& p, int tk, int32_t* pre
   }
   if (threadIdx.x == 0) pre[kv.nseq] = base;
   __syncthreads();
-  return align ? align : max((int64_t)MIN_TILES, div_floor((int64_t)base * p.U + p.grid - 1, p.grid));
+  return align ? align : max((int64_t)MIN_TILES, div_floor((int64_t)base * p.F + p.groups - 1, p.groups));
 }
 
 // sum of 2^(x - lse2) over the first n of V heads (the others are padding); an empty row, of x = -inf
@@ -676,13 +682,13 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
       for (int i = threadIdx.x; i <= p.kv.nseq; i += NTHR) p.pre[i] = pre[i];
       if (threadIdx.x == 0) *p.per = per;
     }
-    const int64_t total = (int64_t)pre[p.kv.nseq] * p.U;
-    x = per * blockIdx.x;
+    const int64_t total = (int64_t)pre[p.kv.nseq] * p.F;
+    x = per * (blockIdx.x / p.P);
     end = min(total, x + per);
     int hi = p.kv.nseq;  // the sequence whose stretch holds x
     while (hi - s > 1) {
       const int mid = (s + hi) >> 1;
-      if ((int64_t)pre[mid] * p.U <= x) s = mid; else hi = mid;
+      if ((int64_t)pre[mid] * p.F <= x) s = mid; else hi = mid;
     }
   }
   while (x < end) {
@@ -699,15 +705,16 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
       ++x;
     } else {
       const int nt = pre[s + 1] - pre[s];
-      const int64_t rel = x - (int64_t)pre[s] * p.U;
-      ui = (int)div_floor(rel, nt);
-      u.t0 = (int)(rel - (int64_t)ui * nt);
+      const int64_t rel = x - (int64_t)pre[s] * p.F;
+      const int bundle = (int)div_floor(rel, nt);
+      ui = bundle * p.P + (int)(blockIdx.x % p.P);
+      u.t0 = (int)(rel - (int64_t)bundle * nt);
       const int to = (int)min((int64_t)nt, u.t0 + (end - x));
       u.t1 = min(to, tiles_of(u.len, Core::TK));  // past it the stretch is rounded up
       begins = u.t0 == 0;
       whole = begins && to == nt;
       x += to - u.t0;
-      if (ui == p.U - 1 && to == nt) ++s;
+      if (bundle == p.F - 1 && to == nt) ++s;
     }
     u.hk = ui / p.hb;
     const int in_group = (ui - u.hk * p.hb) * Core::HT;
@@ -761,20 +768,20 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
   }
 }
 
-// Parts of one unit: CTAs c0 .. c1 hold one each when c0 < c1; c0 == c1 when one CTA finished it.
+// Parts of one unit: n CTAs, P apart, hold one each; n is 1 when one CTA finished it.
 struct Parts {
-  int64_t c0;
-  int n;  // c1 - c0 + 1
-  __device__ int64_t slot(int k) const { return 2 * (c0 + k) + (k == 0); }
+  int first, P, n;
+  __device__ int slot(int k) const { return 2 * (first + k * P) + (k == 0); }
 };
 
 __device__ __forceinline__ Parts unit_parts(const DecodeParams& p, int s, int ui) {
-  if (p.whole) return {0, 1};
+  if (p.whole) return {0, 1, 1};
   const int before = p.pre[s], nt = p.pre[s + 1] - before;
   const int64_t per = *p.per;
-  const int64_t at = (int64_t)before * p.U + (int64_t)ui * nt;
-  const int64_t c0 = div_floor(at, per);
-  return {c0, (int)(div_floor(at + nt - 1, per) - c0) + 1};
+  const int bundle = ui / p.P;
+  const int64_t at = (int64_t)before * p.F + (int64_t)bundle * nt;
+  const int g0 = (int)div_floor(at, per);
+  return {g0 * p.P + (ui - bundle * p.P), p.P, (int)div_floor(at + nt - 1, per) - g0 + 1};
 }
 
 // m (0 for an empty row) and l of head h over the parts: one warp, the same in every lane
@@ -799,9 +806,9 @@ __device__ __forceinline__ void add_parts(const DecodeParams& p, const Parts& u,
                                           int first, int step, float4& a) {
 #pragma unroll 4
   for (int k = first; k < u.n; k += step) {
-    const int64_t at = u.slot(k) * HT + h;
+    const int at = u.slot(k) * HT + h;
     const float f = ex2(p.part_ml[at].x - mu);
-    const float4 v = reinterpret_cast<const float4*>(p.part_O + at * p.d)[column];
+    const float4 v = reinterpret_cast<const float4*>(p.part_O + (int64_t)at * p.d)[column];
     a.x = fmaf(f, v.x, a.x);
     a.y = fmaf(f, v.y, a.y);
     a.z = fmaf(f, v.z, a.z);
@@ -963,17 +970,23 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   if (e0 != cudaSuccess) return e0;
 
   cudaError_t err = cudaSuccess;
+  int grid = 0;
   auto launch = [&](auto core) {
     using Core = decltype(core);
     const int resident = std::min(MAX_GRID, sms * Core::CTAS), units = p.kv.nseq * p.U;
     p.whole = d.kv.max_len <= whole_keys(d, units > resident);
     p.own_scores = p.whole && p.S && p.hb == 1;
-    p.grid = p.whole ? units : resident;
+    // the widest bundle whose groups of CTAs leave few of the resident ones without work
+    p.P = p.U;
+    while (p.U % p.P || 20 * (resident / p.P * p.P) < 19 * resident) --p.P;  // 1 leaves none
+    p.F = p.U / p.P;
+    p.groups = resident / p.P;
+    grid = p.whole ? units : p.groups * p.P;
     const size_t smem = (size_t)WARPS * Core::STAGES * Core::TILE + (p.whole ? 0 : 4 * ((size_t)p.kv.nseq + 1));
     // room for the scan of the largest batch
     err = allow_smem<&k_decode<Core>>(dev, WARPS * Core::STAGES * Core::TILE + 4 * (MAX_SEQS + 1));
     if (err != cudaSuccess) return;
-    k_decode<Core><<<p.grid, NTHR, smem, st>>>(p);
+    k_decode<Core><<<grid, NTHR, smem, st>>>(p);
     err = cudaGetLastError();
   };
   const int D = p.d <= 64 ? 64 : p.d <= 128 ? 128 : p.d <= 192 ? 192 : 256;
@@ -997,7 +1010,7 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
 
   cudaLaunchConfig_t cfg{};
   // parts of a row if all were equally long: from 8 on its join is split over a CTA's warps
-  const int many = p.grid >= 8 * p.kv.nseq * p.U;
+  const int many = grid >= 8 * p.kv.nseq * p.U;
   const int joiners = p.whole ? 0 : std::min(MAX_JOINERS, many ? p.kv.nseq * p.h_r : (p.kv.nseq * p.h_r + 7) / 8);
   const int chunks = p.score_out ? (p.kv.max_len + JOIN_KEYS - 1) / JOIN_KEYS : 0;
   const int adders = chunks * p.kv.nseq * p.h_kv;

@@ -769,3 +769,23 @@ def test_calls_on_a_stream_that_is_not_current():
     assert ((score.double().cpu() - want).abs() <= (64 + 4 + 2 + 8) * 2.0 ** -23 * mag + 1e-30).all()
     torch.cuda.synchronize()
     _clean(mf)
+
+
+@pytest.mark.parametrize("lens,h_kv,group,d,dtype", [
+    ((5, 0, 33, 1), 2, 4, 128, BF), ((16, 64, 65, 130), 3, 3, 80, BF), ((9, 40, 0, 3), 1, 20, 96, BF),
+    ((7, 8, 9, 0), 2, 5, 72, F32), ((200, 1, 64, 500), 2, 4, 96, F32), ((63,), 1, 12, 64, F32),
+    (tuple(range(0, 150)), 4, 2, 64, BF), ((400,) * 40, 2, 1, 104, F32)])
+def test_decode_short_sequences_under_a_long_bound(lens, h_kv, group, d, dtype):
+    """The length bound of a serving loop is far above the lengths: the keys are split all the same,
+    into units of their own where there are few, and the weights go through the second kernel."""
+    mf = _mf()
+    c, _ = ref.make_cache(lens, h_kv, d, 16, dtype, seed=d, stale=float("nan"))
+    Q = torch.randn(len(lens), h_kv * group, d, generator=torch.Generator().manual_seed(4)).to(dtype)
+    kv = _kv(mf, c, max_len=6000)
+    before = torch.rand(len(lens), h_kv, 6000, generator=torch.Generator().manual_seed(5)).cuda()
+    after = before.clone()
+    lse = torch.empty(len(lens), h_kv * group, device="cuda")
+    O = mf.mf_paged_decode(kv, Q.cuda(), lse=lse, score=after)
+    _clean(mf)
+    check_decode(c, Q, O, lse, (before, after))
+    assert torch.equal(O, mf.mf_paged_decode(kv, Q.cuda()))
