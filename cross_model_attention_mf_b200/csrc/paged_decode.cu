@@ -37,7 +37,8 @@ constexpr int MIN_TILES = WARPS;  // tiles a CTA takes at least: one per warp
 constexpr int ALIGN = WARPS;      // ALIGN, 2 ALIGN or 4 ALIGN tiles to a CTA where units have their own
 constexpr int MAX_SEQS = 4096;    // as the entry point checks
 constexpr int JOIN_THR = 256;
-constexpr int JOIN_KEYS = 2048;   // keys whose weights a CTA of the join kernel adds up
+constexpr int JOIN_KEYS = 1024;   // keys whose weights a CTA of the join kernel adds up at a time
+constexpr int JOIN_CTAS = 4;      // its CTAs on an SM
 constexpr int MAX_JOINERS = 2048; // CTAs of the join kernel that add up parts
 constexpr float LN2 = 0.693147180559945309f;
 
@@ -827,8 +828,8 @@ __device__ __forceinline__ void write_row(const DecodeParams& p, int row, int co
 // add them up over the group.  The others add up the parts of the units that were cut: a warp
 // takes a query head, or with `many` parts to a row a CTA does, in slices of the parts that are
 // added up in order.  Both find the row's lse from the parts' (m, l), lanes over parts.
-__global__ void __launch_bounds__(JOIN_THR, 4) k_decode_join(const __grid_constant__ DecodeParams p, int HT, int adders,
-                                                             int many) {
+__global__ void __launch_bounds__(JOIN_THR, JOIN_CTAS) k_decode_join(const __grid_constant__ DecodeParams p, int HT,
+                                                                     int adders, int keys, int many) {
   __shared__ float s_lse2[256];
   __shared__ float4 s_acc[JOIN_THR];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -872,7 +873,7 @@ __global__ void __launch_bounds__(JOIN_THR, 4) k_decode_join(const __grid_consta
   const int chunk = job / rows, sg = job - chunk * rows;
   const int s = sg / p.h_kv, hk = sg - s * p.h_kv;
   const int len = kv_len(p.kv, s, false);
-  const int64_t j0 = (int64_t)chunk * JOIN_KEYS;
+  const int64_t j0 = (int64_t)chunk * keys;
   if (j0 >= len) return;
   auto ready = [&] {  // lse2 of the group's heads (0 for an empty row)
     for (int h = warp; h < p.G; h += JOIN_THR / 32) {
@@ -889,7 +890,7 @@ __global__ void __launch_bounds__(JOIN_THR, 4) k_decode_join(const __grid_consta
     }
     __syncthreads();
   };
-  const int j1 = (int)min((int64_t)len, j0 + JOIN_KEYS);
+  const int j1 = (int)min((int64_t)len, j0 + keys);
   if (p.GP % 4 == 0) add_weights<4, JOIN_THR>(p, sg, (int)j0, j1, s_lse2, ready);
   else add_weights<2, JOIN_THR>(p, sg, (int)j0, j1, s_lse2, ready);
 }
@@ -1012,8 +1013,11 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   // parts of a row if all were equally long: from 8 on its join is split over a CTA's warps
   const int many = grid >= 8 * p.kv.nseq * p.U;
   const int joiners = p.whole ? 0 : std::min(MAX_JOINERS, many ? p.kv.nseq * p.h_r : (p.kv.nseq * p.h_r + 7) / 8);
-  const int chunks = p.score_out ? (p.kv.max_len + JOIN_KEYS - 1) / JOIN_KEYS : 0;
-  const int adders = chunks * p.kv.nseq * p.h_kv;
+  // keys of an adder: the adders fill the GPU once, since each looks its row up first
+  const int rows = p.kv.nseq * p.h_kv;
+  const int64_t share = p.kv.max_len / std::max(1, JOIN_CTAS * sms / rows);
+  const int keys = (int)std::max<int64_t>(1, (share + JOIN_KEYS - 1) / JOIN_KEYS) * JOIN_KEYS;
+  const int adders = p.score_out ? (int)(((int64_t)p.kv.max_len + keys - 1) / keys) * rows : 0;
   cfg.gridDim = dim3((unsigned)adders + (unsigned)joiners);
   if (cfg.gridDim.x == 0) return cudaSuccess;
   cfg.blockDim = dim3(JOIN_THR);
@@ -1023,7 +1027,7 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_decode_join, p, HT, adders, many);
+  return cudaLaunchKernelEx(&cfg, k_decode_join, p, HT, adders, keys, many);
 }
 
 }  // namespace mfi
