@@ -247,6 +247,8 @@ mf_status check_kv(const mf_paged_kv& k) {
   const int64_t e = k.dtype == MF_F32 ? 4 : 2;
   if (bad_stride(k.page_stride, (int64_t)k.page_size * k.h_kv * k.d, e))
     return fail(MF_ERR_INVALID, "page_stride must be 0, or cover a page in a multiple of 16 bytes");
+  if (k.page_stride > (int64_t)1 << 28 && k.page_stride > ((int64_t)1 << 60) / k.n_pages)
+    return fail(MF_ERR_UNSUPPORTED, "n_pages * page_stride does not fit 64-bit offsets");
   if (misaligned(k.K, 16) || misaligned(k.V, 16)) return fail(MF_ERR_INVALID, "K and V must be 16-byte aligned");
   if (misaligned(k.block_table, 4) || misaligned(k.seq_lens, 4)) return fail(MF_ERR_INVALID, "block_table and seq_lens must be 4-byte aligned");
   return MF_OK;

@@ -789,3 +789,157 @@ def test_decode_short_sequences_under_a_long_bound(lens, h_kv, group, d, dtype):
     _clean(mf)
     check_decode(c, Q, O, lse, (before, after))
     assert torch.equal(O, mf.mf_paged_decode(kv, Q.cuda()))
+
+
+# ------------------------------------------------------------------ borders
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_nothing_held(dtype):
+    """max_len 0: every call succeeds, empty rows get O = 0 and lse = -inf, nothing else changes."""
+    mf = _mf()
+    K, V = torch.ones(2, 4, 2, 64, device="cuda").to(dtype), torch.ones(2, 4, 2, 64, device="cuda").to(dtype)
+    kv = mf.PagedKV(K, V, torch.full((3, 1), -1, dtype=torch.int32, device="cuda"),
+                    torch.zeros(3, dtype=torch.int32, device="cuda"), 0)
+    for G in (1, 4, 20):
+        lse = torch.zeros(3, 2 * G, device="cuda")
+        score = torch.full((3, 2, 1), 5.0, device="cuda")
+        O = mf.mf_paged_decode(kv, torch.ones(3, 2 * G, 64, device="cuda").to(dtype), lse=lse, score=score)
+        _clean(mf)
+        assert (O == 0).all() and (lse == -math.inf).all() and (score == 5.0).all()
+    pos = torch.full((3, 2, 1), 7, dtype=torch.int32, device="cuda")
+    mf.mf_kv_append(kv, K[0, :0], V[0, :0], torch.zeros(4, dtype=torch.int32, device="cuda"), 0, score=score, pos=pos)
+    out = mf.mf_kv_evict(kv, score, pos, 3)
+    _clean(mf)
+    assert out.tolist() == [0, 0, 0] and (score == 5.0).all() and (pos == 7).all() and (K == 1).all() and (V == 1).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_largest_batch(dtype):
+    """4096 sequences, with the keys split and with a CTA to a unit."""
+    mf = _mf()
+    n, page, d = 4096, 4, 64
+    g = torch.Generator().manual_seed(6)
+    lens = torch.randint(0, 9, (n,), generator=g).tolist()
+    lens[7], lens[4095] = 700, 40
+    K, V = (torch.randn(300, page, 1, d, generator=g).to(dtype) for _ in range(2))
+    table = torch.randint(0, 300, (n, 175), generator=g).to(torch.int32)
+    c = ref.Cache(K, V, table, lens, page)
+    Q = torch.randn(n, 2, d, generator=g).to(dtype)
+    kv = mf.PagedKV(K.cuda(), V.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), 700)
+    lse = torch.empty(n, 2, device="cuda")
+    O = mf.mf_paged_decode(kv, Q.cuda(), lse=lse)
+    _clean(mf)
+    check_decode(c, Q, O, lse)
+    c.lens = [min(L, 40) for L in lens]
+    kv.seq_lens.clamp_(max=40)
+    kv.max_len = 40
+    before = torch.zeros(n, 1, 40, device="cuda")
+    after = before.clone()
+    O = mf.mf_paged_decode(kv, Q.cuda(), score=after)
+    _clean(mf)
+    check_decode(c, Q, O, None, (before, after))
+
+
+@pytest.mark.parametrize("lens,h_kv,group,dtype", [((300, 17), 1, 256, BF), ((100,), 1, 256, F32), ((250, 40, 3), 2, 20, BF),
+                                                   ((120, 9), 3, 9, F32), ((511, 512), 64, 4, BF), ((900,), 64, 2, F32)])
+def test_decode_many_heads(lens, h_kv, group, dtype):
+    """Groups of several blocks of heads, with and without a second launch; 64 key heads."""
+    mf = _mf()
+    c, _ = ref.make_cache(lens, h_kv, 64, 16, dtype, seed=group, stale=float("nan"))
+    Q = torch.randn(len(lens), h_kv * group, 64, generator=torch.Generator().manual_seed(4)).to(dtype)
+    for top in (max(lens), 3000):
+        kv = _kv(mf, c, max_len=top)
+        before = torch.rand(len(lens), h_kv, top, generator=torch.Generator().manual_seed(5)).cuda()
+        after = before.clone()
+        lse = torch.empty(len(lens), h_kv * group, device="cuda")
+        O = mf.mf_paged_decode(kv, Q.cuda(), lse=lse, score=after)
+        _clean(mf)
+        check_decode(c, Q, O, lse, (before, after))
+
+
+def test_evict_extreme_positions():
+    """Windows and positions at the ends of 32 bits."""
+    mf = _mf()
+    top, low = 2 ** 31 - 1, -2 ** 31
+    for seen, sink, window in ((low, 0, 5), (top, 3, 5), (5, 0, 0), (0, 2, 5), (low, 4, 0)):
+        c, _ = ref.make_cache((50,), 1, 64, 16, F32, seed=9)
+        kv = _kv(mf, c)
+        g = torch.Generator().manual_seed(1)
+        score = torch.rand(1, 1, 50, generator=g)
+        pos = torch.tensor([low, low + 1, -1, 0, 1, 2, top - 4, top - 1, top] + list(range(10, 51)), dtype=torch.int32)[None, None].contiguous()
+        sd, pd = score.cuda(), pos.cuda()
+        mf.mf_kv_evict(kv, sd, pd, 20, sink=sink, window=window, n_seen=torch.tensor([seen], dtype=torch.int32, device="cuda"))
+        _clean(mf)
+        wscore, wpos, wlens = ref.evict(c, score, pos, [seen], 20, sink, window)
+        assert kv.seq_lens.tolist() == wlens
+        assert torch.equal(sd.cpu(), wscore) and torch.equal(pd.cpu(), wpos) and torch.equal(kv.K.cpu(), c.K)
+
+
+def test_evict_reports_bad_lengths_and_pages():
+    """A length out of range counts as the nearest bound; rows on a page that does not exist read as
+    zeros and are not written."""
+    mf = _mf()
+    c, _ = ref.make_cache((40, 40), 1, 64, 16, F32, seed=3)
+    kv = _kv(mf, c)
+    score = torch.arange(40).float().expand(2, 1, 40).contiguous()
+    pos = torch.arange(40, dtype=torch.int32).expand(2, 1, 40).contiguous()
+    sd, pd = score.cuda(), pos.cuda()
+    kv.seq_lens = torch.tensor([55, -2], dtype=torch.int32, device="cuda")
+    mf.mf_kv_evict(kv, sd, pd, 10)
+    assert mf.mf_get_status() == (mf.MF_ERR_DEVICE_INDEX, 1)
+    wscore, wpos, _ = ref.evict(ref.Cache(c.K, c.V, c.table, [40, 0], c.page), score, pos, [40, 0], 10, 0, 0)
+    assert kv.seq_lens.tolist() == [10, 0]
+    assert torch.equal(sd.cpu(), wscore) and torch.equal(pd.cpu(), wpos) and torch.equal(kv.K.cpu(), c.K)
+    # the movers' page is missing: they arrive as zeros
+    c, _ = ref.make_cache((40,), 1, 64, 16, F32, seed=3)
+    kv = _kv(mf, c)
+    kv.block_table[0, 2] = 99
+    sd, pd = score[:1].cuda(), pos[:1].cuda()
+    K0 = kv.K.clone()
+    mf.mf_kv_evict(kv, sd, pd, 10)
+    assert mf.mf_get_status() == (mf.MF_ERR_DEVICE_INDEX, 16)
+    first = c.table[0, 0].item()
+    got = kv.K.cpu()
+    # kept: slots 30 .. 39; 30 and 31 lie on the second page, 32 .. 39 on the missing one
+    assert torch.equal(got[first, 0], K0.cpu()[c.table[0, 1].item(), 14]) and torch.equal(got[first, 1], K0.cpu()[c.table[0, 1].item(), 15])
+    assert (got[first, 2:10] == 0).all() and pd[0, 0, :10].tolist() == list(range(30, 40))
+    got[first, :10] = K0.cpu()[first, :10]
+    assert torch.equal(got, K0.cpu())
+
+
+def test_pages_beyond_four_gigabytes():
+    """Rows whose offsets pass 32 bits, in bytes and in elements: append, decode and eviction on the
+    last pages of a pool of 9 GB for K and for V."""
+    mf = _mf()
+    page, h_kv, d, n_pages = 16, 8, 128, 280000
+    K, V = (torch.empty(n_pages, page, h_kv, d, dtype=BF, device="cuda") for _ in range(2))
+    assert K.numel() > 2 ** 32
+    small, _ = ref.make_cache((70, 33), h_kv, d, page, BF, seed=17, spare=0)
+    n = small.K.shape[0]
+    first = n_pages - n
+    K[:n].zero_(), V[:n].zero_()
+    table = torch.where(small.table >= 0, small.table + first, small.table).cuda()
+    kv = mf.PagedKV(K, V, table, torch.tensor(small.lens, dtype=torch.int32, device="cuda"), 70)
+    idx = [(small.table[s].long()[torch.arange(L) // page], torch.arange(L) % page) for s, L in enumerate(small.lens)]
+    Kn, Vn = (torch.cat([t[i] for i in idx]).cuda() for t in (small.K, small.V))
+    score, pos = torch.rand(2, h_kv, 70, device="cuda"), torch.zeros(2, h_kv, 70, dtype=torch.int32, device="cuda")
+    mf.mf_kv_append(kv, Kn, Vn, torch.tensor([0, 70, 103], dtype=torch.int32, device="cuda"), 70, score=score, pos=pos)
+    Q = torch.randn(2, 4 * h_kv, d, generator=torch.Generator().manual_seed(2)).to(BF)
+    check_decode(small, Q, mf.mf_paged_decode(kv, Q.cuda(), score=score))
+    kv.max_len = 4000  # split
+    wide = torch.zeros(2, h_kv, 4000, device="cuda")
+    check_decode(small, Q, mf.mf_paged_decode(kv, Q.cuda(), score=wide), None, (torch.zeros_like(wide), wide))
+    before = score.cpu()
+    kv.max_len = 70
+    mf.mf_kv_evict(kv, score, pos, 40, 2, 8)
+    _clean(mf)
+    hpos = torch.zeros(2, h_kv, 70, dtype=torch.int32)
+    for s, L in enumerate(small.lens):
+        hpos[s, :, :L] = torch.arange(L, dtype=torch.int32)
+    wscore, wpos, wlens = ref.evict(small, before, hpos, [70, 33], 40, 2, 8)
+    assert kv.seq_lens.tolist() == wlens and torch.equal(score.cpu(), wscore) and torch.equal(pos.cpu(), wpos)
+    for s, L in enumerate(wlens):
+        p, r = small.table[s].long()[torch.arange(L) // page], torch.arange(L) % page
+        assert torch.equal(K[(p + first).cuda(), r.cuda()].cpu(), small.K[p, r])
+        assert torch.equal(V[(p + first).cuda(), r.cuda()].cpu(), small.V[p, r])
+    assert (K[:n] == 0).all() and (V[:n] == 0).all()

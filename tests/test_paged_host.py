@@ -81,7 +81,13 @@ KV_BAD = [("K", 0, 1), ("V", 0, 1), ("block_table", 0, 1), ("seq_lens", 0, 1), (
           ("h_kv", 0, 1), ("d", 0, 1), ("nseq", 4097, 2), ("max_len", 1 << 30, 2), ("h_kv", 65, 2),
           ("d", 20, 2), ("d", 264, 2), ("page_stride", 16 * 2 * 64 - 8, 1),
           ("page_stride", 16 * 2 * 64 + 4, 1), ("page_stride", -8, 1), ("K", A + 8, 1), ("V", A + 2, 1),
-          ("seq_lens", A + 1, 1)]
+          ("seq_lens", A + 1, 1), ("page_stride", (1 << 58) - 8, 1), ("page_stride", (1 << 56) + 8, 1)]
+
+
+def test_page_offsets_that_pass_64_bits_are_refused(mf):
+    d = decode_desc(mf)
+    d.kv.page_stride, d.kv.n_pages = 1 << 50, 1 << 20
+    assert call(mf, "mf_paged_decode", d) == 2
 
 
 @pytest.mark.parametrize("name", ["mf_paged_decode", "mf_kv_append", "mf_kv_evict"])
