@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(CS_THR, CS_CTAS) k_colsum(const __grid_constan
   float* acc = wg + p.h_s * p.h_kv;        // [h_kv][B]
   float* col = acc + p.h_kv * B;           // [CS_HEADS][B]
   __shared__ uint32_t s_lo, s_hi;          // least and largest (query block, live rows) that a sequence gives the row
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  await_earlier();
+  allow_later();  // k_colmerge reads the maps' indices before it waits: not before this kernel may
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t nb = block_count(p, blockIdx.x == 0 && tid == 0);
   const int64_t per = tiles_per_cta(nb, p.h_s, p.grid);
@@ -232,9 +233,13 @@ __global__ void __launch_bounds__(CM_THR) k_colmerge(const __grid_constant__ Col
   const int nq = (int)(((int64_t)L + B - 1) / B);
   if (L < 0 || L > p.max_len || b < 0 || (int64_t)b + nq > p.n_rows) {
     if (kb == 0 && tid == 0) atomicOr(p.status, ST_INDEX);
+    await_earlier();
     return;
   }
-  if (kb >= nq) return;
+  if (kb >= nq) {
+    await_earlier();
+    return;
+  }
   const int64_t nb = block_count(p, false);
   const int64_t per = tiles_per_cta(nb, p.h_s, p.grid);
   const int room = merge_list(p.nqb_max, p.grid);
@@ -278,7 +283,7 @@ __global__ void __launch_bounds__(CM_THR) k_colmerge(const __grid_constant__ Col
     __syncthreads();
   }
   count = min(count, room);  // more only if rows overlap, which is reported above
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  await_earlier();
   // a thread takes four columns of the key head's row; h_kv B is a multiple of 32
   const int cols = p.h_kv * B / 4;
   const int ns = cols >= CM_THR ? 1 : CM_THR / cols;  // slices of the list
@@ -358,8 +363,7 @@ cudaError_t launch_key_scores(const mf_key_scores_desc& d, const KeyScoresWs& ws
   auto launch = [&](auto kern) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return;
-    kern<<<p.grid, CS_THR, smem, st>>>(p);
-    e = cudaGetLastError();
+    e = launch_early(kern, p.grid, CS_THR, smem, 1, st, p);
   };
   if (d.map_dtype == MF_F32) {
     if (d.B == 32) launch(k_colsum<float, 32>);
@@ -371,17 +375,8 @@ cudaError_t launch_key_scores(const mf_key_scores_desc& d, const KeyScoresWs& ws
     else launch(k_colsum<__nv_bfloat16, 128>);
   }
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
-  cfg.gridDim = dim3((unsigned)((int64_t)p.nseq * p.nqb_max));
-  cfg.blockDim = dim3(CM_THR);
-  cfg.dynamicSmemBytes = 4 * (size_t)merge_list(p.nqb_max, p.grid);
-  cfg.stream = st;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_colmerge, p, d.B);
+  return launch_early(k_colmerge, (unsigned)((int64_t)p.nseq * p.nqb_max), CM_THR, 4 * (size_t)merge_list(p.nqb_max, p.grid), 1,
+                      st, p, d.B);
 }
 
 }  // namespace mfi

@@ -52,6 +52,7 @@ struct AppendParams {
 
 __global__ void __launch_bounds__(AP_THR) k_append(const __grid_constant__ AppendParams p) {
   const int s = blockIdx.x / p.chunks, chunk = blockIdx.x - s * p.chunks;
+  await_earlier();
   const int c0 = p.cu[s], n = p.cu[s + 1] - c0;
   const int len = kv_len(p.kv, s, chunk == 0 && threadIdx.x == 0);
   if (n < 0 || n > p.max_new || n > len || c0 < 0 || (int64_t)c0 + n > p.total_new) {
@@ -168,12 +169,12 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
   const int s = job / p.h_kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool first = job == s * p.h_kv && rank == 0 && tid == 0;
-  // the move kernel may take its place; it waits for this grid before its first access
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int seen = p.n_seen ? p.n_seen[s] : 0;
-  const int len = kv_len(p.kv, s, first);
   for (int i = tid; i < 2 * BINS / 4; i += THR) reinterpret_cast<uint4*>(s_hist)[i] = make_uint4(0, 0, 0, 0);
   if (tid < 4) s_tot[tid] = 0;
+  await_earlier();
+  allow_later();
+  const int seen = p.n_seen ? p.n_seen[s] : 0;
+  const int len = kv_len(p.kv, s, first);
   // a bound below -2^31 protects every slot, as -2^31 does
   const int recent = (int)max((int64_t)INT32_MIN, (int64_t)(p.n_seen ? seen : len) - p.window);
   const int left = min(len, p.budget);
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(MV_THR, 4) k_evict_move(const __grid_constant_
   const int job = blockIdx.x / chunks, chunk = blockIdx.x - job * chunks;
   const int s = job / p.h_kv, g = job - s * p.h_kv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  await_earlier();
   if (chunk == 0 && g == 0 && threadIdx.x == 0) p.lens_out[s] = p.ws.len[s];
   const int m0 = chunk * MV_CHUNK + warp * MV_ROWS;
   const int rows = min(MV_ROWS, p.ws.count[job] - m0);
@@ -496,8 +497,7 @@ cudaError_t launch_kv_append(const mf_kv_append_desc& d, uint32_t* status, cudaS
   p.h_kv = d.kv.h_kv;
   p.toks = std::max(1, AP_VECS / (p.kv.slot_bytes / 16));
   p.chunks = std::max(1, (d.max_new + p.toks - 1) / p.toks);
-  k_append<<<(unsigned)((int64_t)p.chunks * d.kv.nseq), AP_THR, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_early(k_append, (unsigned)((int64_t)p.chunks * d.kv.nseq), AP_THR, 0, 1, st, p);
 }
 
 size_t kv_evict_ws(const mf_kv_evict_desc& d, KvEvictWs* ws, void* base) {
@@ -551,22 +551,11 @@ cudaError_t launch_kv_evict(const mf_kv_evict_desc& d, const KvEvictWs& ws, uint
                             (d.kv.max_len > 2 * EV_SLOTS && (int64_t)C * EV_SLOTS < d.kv.max_len &&
                              2 * (int64_t)C * jobs <= sms))) C *= 2;
   const int keys = (int)std::min<int64_t>(32 * thr, ((int64_t)d.kv.max_len + C - 1) / C);
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
-  cfg.gridDim = dim3((unsigned)((int64_t)jobs * C));
-  cfg.blockDim = dim3(thr);
-  cfg.dynamicSmemBytes = (4 * (size_t)keys + 15) & ~size_t(15);
-  cfg.stream = st;
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)C;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = C > 1 ? 1 : 0;
+  const size_t smem = (4 * (size_t)keys + 15) & ~size_t(15);
   auto launch = [&](auto kernel) {
     constexpr auto K = decltype(kernel)::value;
     e = allow_smem<K>(dev, 4 * 32 * EV_WIDE);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, K, p);
+    if (e == cudaSuccess) e = launch_early(K, (unsigned)((int64_t)jobs * C), thr, smem, C, st, p);
   };
   using std::integral_constant;
   if (C == 1 && thr == EV_WIDE) launch(integral_constant<void (*)(EvictParams), &k_evict_select<EV_WIDE, true>>{});
@@ -575,16 +564,7 @@ cudaError_t launch_kv_evict(const mf_kv_evict_desc& d, const KvEvictWs& ws, uint
   if (e != cudaSuccess) return e;
 
   const int chunks = (int)std::max<int64_t>(1, (ws.moves + MV_CHUNK - 1) / MV_CHUNK);
-  cudaLaunchConfig_t mv{};
-  mv.gridDim = dim3((unsigned)((int64_t)jobs * chunks));
-  mv.blockDim = dim3(MV_THR);
-  mv.stream = st;
-  cudaLaunchAttribute pa[1];
-  pa[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pa[0].val.programmaticStreamSerializationAllowed = 1;
-  mv.attrs = pa;
-  mv.numAttrs = 1;
-  return cudaLaunchKernelEx(&mv, k_evict_move, p, chunks);
+  return launch_early(k_evict_move, (unsigned)((int64_t)jobs * chunks), MV_THR, 0, 1, st, p, chunks);
 }
 
 }  // namespace mfi

@@ -668,8 +668,8 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
   uint8_t* ring = smem + warp * RING;
   int32_t* pre = reinterpret_cast<int32_t*>(smem + WARPS * RING);
 
-  // the join kernel may take its place now; it waits for this grid before its first access
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  await_earlier();
+  if (!p.whole || (p.S && !p.own_scores)) allow_later();  // k_decode_join follows
   int64_t x, end;
   int s = 0;
   if (p.whole) {
@@ -833,7 +833,7 @@ __global__ void __launch_bounds__(JOIN_THR, JOIN_CTAS) k_decode_join(const __gri
   __shared__ float s_lse2[256];
   __shared__ float4 s_acc[JOIN_THR];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  await_earlier();
   if ((int)blockIdx.x >= adders) {
     const int nc = p.d >> 2, ns = JOIN_THR / nc;  // 16-byte columns of a row, slices
     const int per = many ? 1 : JOIN_THR / 32;     // rows a CTA takes at a time
@@ -987,8 +987,7 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
     // room for the scan of the largest batch
     err = allow_smem<&k_decode<Core>>(dev, WARPS * Core::STAGES * Core::TILE + 4 * (MAX_SEQS + 1));
     if (err != cudaSuccess) return;
-    k_decode<Core><<<grid, NTHR, smem, st>>>(p);
-    err = cudaGetLastError();
+    err = launch_early(k_decode<Core>, grid, NTHR, smem, 1, st, p);
   };
   const int D = p.d <= 64 ? 64 : p.d <= 128 ? 128 : p.d <= 192 ? 192 : 256;
   if (d.kv.dtype == MF_F32) {
@@ -1009,7 +1008,6 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   }
   if (err != cudaSuccess || (p.whole && (!p.score_out || p.own_scores))) return err;
 
-  cudaLaunchConfig_t cfg{};
   // parts of a row if all were equally long: from 8 on its join is split over a CTA's warps
   const int many = grid >= 8 * p.kv.nseq * p.U;
   const int joiners = p.whole ? 0 : std::min(MAX_JOINERS, many ? p.kv.nseq * p.h_r : (p.kv.nseq * p.h_r + 7) / 8);
@@ -1018,16 +1016,9 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
   const int64_t share = p.kv.max_len / std::max(1, JOIN_CTAS * sms / rows);
   const int keys = (int)std::max<int64_t>(1, (share + JOIN_KEYS - 1) / JOIN_KEYS) * JOIN_KEYS;
   const int adders = p.score_out ? (int)(((int64_t)p.kv.max_len + keys - 1) / keys) * rows : 0;
-  cfg.gridDim = dim3((unsigned)adders + (unsigned)joiners);
-  if (cfg.gridDim.x == 0) return cudaSuccess;
-  cfg.blockDim = dim3(JOIN_THR);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_decode_join, p, HT, adders, keys, many);
+  const unsigned ctas = (unsigned)adders + (unsigned)joiners;
+  if (ctas == 0) return cudaSuccess;
+  return launch_early(k_decode_join, ctas, JOIN_THR, 0, 1, st, p, HT, adders, keys, many);
 }
 
 }  // namespace mfi

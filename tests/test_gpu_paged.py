@@ -943,3 +943,112 @@ def test_pages_beyond_four_gigabytes():
         assert torch.equal(K[(p + first).cuda(), r.cuda()].cpu(), small.K[p, r])
         assert torch.equal(V[(p + first).cuda(), r.cuda()].cpu(), small.V[p, r])
     assert (K[:n] == 0).all() and (V[:n] == 0).all()
+
+
+# ------------------------------------------------------------------ order among kernels
+
+def _order_case(mf):
+    """The four calls over one cache, and what they read, as one list of tensors."""
+    lens, h_kv, G, d, page, cap = [600, 77, 1, 0], 2, 4, 64, 16, 640
+    c, _ = ref.make_cache(lens, h_kv, d, page, BF, seed=41, capacity=[cap] * 4)
+    kv = _kv(mf, c, max_len=cap)
+    g = torch.Generator().manual_seed(8)
+    Q, Kn, Vn = (torch.randn(4, n, d, generator=g).to(BF).cuda() for n in (h_kv * G, h_kv, h_kv))
+    score = torch.rand(4, h_kv, cap, generator=g).cuda()
+    pos = torch.arange(cap, dtype=torch.int32, device="cuda").expand(4, h_kv, cap).contiguous()
+    seen = kv.seq_lens.clone()
+    values, row_ptr, cols, base = ref.make_bsr((600, 77, 1), 64, 4, BF, seed=1)
+    bsr = mf.BSR(row_ptr.cuda(), cols.cuda(), values.cuda(), row_ptr[-1:].cuda())
+    W = torch.rand(h_kv * G, 4, generator=g).cuda()
+    cu = torch.tensor([0, 600, 677, 678], dtype=torch.int32, device="cuda")
+    qb = torch.tensor(base, dtype=torch.int32, device="cuda")
+    one = torch.arange(5, dtype=torch.int32, device="cuda")
+    outs = dict(O=torch.zeros(4, h_kv * G, d, device="cuda"), lse=torch.zeros(4, h_kv * G, device="cuda"),
+                keys=torch.zeros(3, h_kv, 600, device="cuda"), so=torch.zeros_like(score), po=torch.zeros_like(pos),
+                lo=torch.zeros_like(kv.seq_lens), after=torch.zeros_like(score))
+    inputs = [kv.K, kv.V, kv.block_table, kv.seq_lens, Q, Kn, Vn, score, pos, seen, bsr.row_ptr, bsr.col_idx, bsr.values, W, cu, qb]
+    ws = torch.empty(max(mf.mf_paged_decode_workspace_size(kv, h_kv * G, True), mf.mf_kv_evict_workspace_size(kv, 64),
+                         mf.mf_map_key_scores_workspace_size(bsr.capacity, 64, h_kv)), dtype=torch.uint8, device="cuda")
+
+    def step():  # one workspace for all: each call may use it once the one before is done
+        kv.seq_lens.add_(1)
+        seen.add_(1)
+        mf.mf_kv_append(kv, Kn, Vn, one, 1, n_seen=seen, score=score, pos=pos)
+        mf.mf_map_key_scores(bsr, W, cu, qb, 600, h_kv, score=outs["keys"], workspace=ws)
+        mf.mf_paged_decode(kv, Q, O=outs["O"], lse=outs["lse"], score=score, score_out=outs["after"], o_f32=True, workspace=ws)
+        mf.mf_kv_evict(kv, outs["after"], pos, 64, 2, 8, n_seen=seen, score_out=outs["so"], pos_out=outs["po"],
+                       seq_lens_out=outs["lo"], workspace=ws)
+    return inputs, outs, step
+
+
+def test_calls_wait_for_what_they_read():
+    """Inputs written by a kernel just before the call, outputs read and overwritten just after it,
+    and two inputs' values in turn: every result equals that of a run with a wait around each call."""
+    mf = _mf()
+    inputs, outs, step = _order_case(mf)
+    first = [t.clone() for t in inputs]
+    second = [t.clone() for t in first]
+    for i in (4, 5, 6, 7, 12, 13):  # Q, new rows, scores, map values, W
+        second[i] = (first[i].float() * 0.5 + 0.1).to(first[i].dtype)
+    want = []
+    for src in (first, second):
+        for t, v in zip(inputs, src):
+            t.copy_(v)
+        torch.cuda.synchronize()
+        for o in outs.values():
+            o.zero_()
+        torch.cuda.synchronize()
+        step()
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in outs.values()] + [inputs[0].clone(), inputs[1].clone()])
+    torch.cuda.synchronize()
+    assert any(not torch.equal(a, b) for a, b in zip(*want))
+    got = []
+    for n in range(40):
+        for t, v in zip(inputs, (first, second)[n % 2]):
+            t.copy_(v)
+        for o in outs.values():
+            o.zero_()
+        step()
+        got.append([o.clone() for o in outs.values()] + [inputs[0].clone(), inputs[1].clone()])
+    torch.cuda.synchronize()
+    _clean(mf)
+    for n, r in enumerate(got):
+        for a, b in zip(r, want[n % 2]):
+            assert torch.equal(a, b), n
+
+
+def test_captured_calls_after_a_joined_stream():
+    """A captured step whose first calls depend on two streams, replayed with new inputs."""
+    mf = _mf()
+    inputs, outs, step = _order_case(mf)
+    first = [t.clone() for t in inputs]
+    for o in outs.values():
+        o.zero_()
+    torch.cuda.synchronize()
+    step()
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs.values()] + [inputs[0].clone()]
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):  # half of the inputs are restored beside the others
+            for t, v in list(zip(inputs, first))[::2]:
+                t.copy_(v)
+        for t, v in list(zip(inputs, first))[1::2]:
+            t.copy_(v)
+        for o in outs.values():
+            o.zero_()
+        main.wait_stream(side)
+        step()
+    for _ in range(5):
+        for t in inputs[4:8]:
+            t.zero_()
+        graph.replay()
+        got = [o.clone() for o in outs.values()] + [inputs[0].clone()]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    _clean(mf)
