@@ -13,6 +13,12 @@
 // k_colmerge CTA (sequence, key block): lists the parts of the block's column in every later
 //            query-block row (binary search of the ascending columns; this runs beside k_colsum),
 //            then adds them in float64, in slices of the list that are joined in order.
+//
+// Measured (one B200; copy rate 6469 GB/s): 1.17 GB of kept blocks (4 sequences, 40 sender heads)
+// 198 us, 91% of that rate (k_colsum 187: masked tiles have a loop of their own, without which it
+// was bound by instructions at 236); 58 MB (8192 tokens, 3% of the blocks) 19.5 us: 4 us until the
+// first block's row is known, 10 for two or three tiles a warp, 3 for the merge.  Three CTAs of
+// k_colsum to an SM: two took 205 us, four (with spills) 197 and 21 for the small case.
 #include <cuda_bf16.h>
 #include <stdint.h>
 

@@ -7,9 +7,9 @@
 // the kept set is the `budget` largest keys, equal keys by slot.  k_evict_select finds the
 // smallest kept key by counting: up to three rounds over 11, 11 and 10 bits, each a histogram of
 // the slots that still share the prefix, walked from the top; a round whose bin is kept whole is
-// the last.  A cluster of CTAs shares one (sequence, key head): the keys stay in its shared
-// memory, the histograms are added over distributed shared memory, so scores and positions are
-// read once before the kept ones are copied.
+// the last.  A CTA, or a cluster of them, has one (sequence, key head): the keys stay in its shared
+// memory, a cluster's histograms are added over distributed shared memory, so scores and positions
+// are read once; outputs that are not the inputs are written from the registers of that read.
 // With kb(j) kept slots before slot j, hole j is the (j - kb(j))-th and mover j the
 // (kb(j) - kb(new length))-th: one count over the cluster places both.
 // What bounds the selection is the number of instructions per slot, next to the latency of a
@@ -18,6 +18,11 @@
 // they are and only the kept rows above it move, into the dropped slots: every source lies at or
 // above the budget and every target below, so all moves are independent and k_evict_move makes
 // them in any order.
+//
+// Measured (one B200; copy rate 6469 GB/s): append of 15938 rows of 8 x 128 bf16 for K and V 26.6 us
+// (92%), of 64 rows 3.4 us (launch); one slot out of each of 512 rows of 2049 12.6 us (the selection
+// 11); 16 prompts of 1024 to 8192 tokens cut to 2048 35.7 us (selection 11, moves 22: 117 MB at 82%);
+// 8 rows of 131072 cut to 16384 44.9 us (selection 22 on 64 SMs, moves 21).
 #include <cooperative_groups.h>
 #include <stdint.h>
 
@@ -50,6 +55,8 @@ struct AppendParams {
   int chunks;
 };
 
+// One 16-byte vector of K and of V per thread and step, four steps in flight; a CTA takes about 16 KB
+// of each, whole tokens.
 __global__ void __launch_bounds__(AP_THR) k_append(const __grid_constant__ AppendParams p) {
   const int s = blockIdx.x / p.chunks, chunk = blockIdx.x - s * p.chunks;
   await_earlier();
@@ -148,6 +155,8 @@ __device__ __forceinline__ uint32_t lowest_bits(uint32_t m, uint32_t n) {
   return r;
 }
 
+// Keys in registers and loops unrolled over a thread's slots took 26 us for 512 rows of 2049 slots:
+// the code left the instruction cache.  Loops over shared memory with few instructions: 12.6.
 // A CTA's slots are one tile of at most 32 THR, whose keys stay in shared memory, or are read
 // again, tile by tile, in every pass.  A warp owns up to 32 groups of 32 neighbouring slots of a
 // tile; ballots mark a group's keys above the bar and at it, and lane q keeps the marks of group

@@ -428,7 +428,8 @@ typedef struct {
  * head g = r / (h_r / h_kv), slots j < seq_lens[s] (the new token's own slot among them):
  *   x_j = scale * q_r . K[j][g],  lse = ln sum_j exp(x_j),  O_r = sum_j exp(x_j - lse) V[j][g].
  * A sequence of length 0 gets O = 0 and lse = -inf, and so does a row whose every x_j is -inf;
- * a NaN or +inf among the x_j makes the row NaN.
+ * a NaN or +inf among the x_j makes the row NaN (O, lse and the weights it adds).  An infinite V
+ * makes its elements of O infinite or NaN.
  * Q: [nseq] rows of [h_r][d], q_stride elements apart (0 = h_r * d; a slice of a fused projection
  * needs no copy).  O: [nseq][h_r][d] in the cache's dtype, or float32 with MF_DECODE_O_F32.  lse
  * (optional): float [nseq][h_r].
@@ -437,9 +438,9 @@ typedef struct {
  * they were.  score_in may be score_out itself; NULL stands for zeros.
  * Arithmetic: bf16 keys and values run on tensor cores with float32 accumulation, the weights
  * taking part as a bf16 pair (hi + lo, ~16 bits); float32 caches run in float32 throughout.
- * Softmax statistics are float32.  The keys are split over the GPU by a rule on nseq, h_kv, the
- * lengths and the number of SMs, and the parts are joined in a fixed order: repeated calls give
- * the same bits.
+ * Softmax statistics are float32.  The keys are split over the GPU by a rule on nseq, h_kv, h_r, d,
+ * max_len, the lengths and the number of SMs, and the parts are joined in a fixed order: repeated
+ * calls give the same bits.
  * Requirements: h_r a multiple of h_kv, h_r <= 256; Q and O 16-byte aligned, q_stride a multiple
  * of 16 bytes; scale finite and >= 0 (0 means 1 / sqrt(d)). */
 #define MF_DECODE_O_F32 1            /* flags: O is float32 */
@@ -531,8 +532,8 @@ mf_status mf_kv_evict(const mf_kv_evict_desc* desc, void* workspace, size_t work
  * repeated calls give the same bits.  A BSR row, column or length out of range sets status bit 1
  * and its blocks are skipped.  Two sequences may name the same BSR rows if they are equally long;
  * otherwise bit 1 is set and the blocks of rows that they hold differently are skipped.
- * Requirements: B in {32, 64, 128}; 1 <= h_s <= 256; h_r a multiple of h_kv, h_kv <= 64; values
- * 16-byte aligned; at most 4096 query blocks per sequence; nseq <= 4096; n_rows < 2^24. */
+ * Requirements: columns ascending within a row, each once, as mf_compress writes them; B in
+ * {32, 64, 128}; 1 <= h_s <= 256; h_r a multiple of h_kv, h_kv <= 64; values 16-byte aligned; at most 4096 query blocks per sequence; nseq <= 4096; n_rows < 2^24. */
 typedef struct {
   mf_bsr bsr;
   int64_t n_rows;                  /* rows of the BSR: row_ptr has n_rows + 1 entries */
