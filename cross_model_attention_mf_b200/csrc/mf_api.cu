@@ -241,7 +241,7 @@ mf_status check_kv(const mf_paged_kv& k) {
   if (k.nseq < 1 || k.max_len < 0) return fail(MF_ERR_INVALID, "nseq must be >= 1 and max_len >= 0");
   if (k.h_kv < 1 || k.d < 1) return fail(MF_ERR_INVALID, "h_kv and d must be >= 1");
   if (k.nseq > 4096) return fail(MF_ERR_UNSUPPORTED, "more than 4096 sequences");
-  if ((int64_t)k.nseq * k.max_len >= (int64_t)1 << 31) return fail(MF_ERR_UNSUPPORTED, "nseq * max_len must be below 2^31");
+  if ((int64_t)k.nseq * k.max_len > (int64_t)1 << 30) return fail(MF_ERR_UNSUPPORTED, "nseq * max_len must be at most 2^30");
   if (k.h_kv > 64) return fail(MF_ERR_UNSUPPORTED, "h_kv must be <= 64");
   if (k.d % 8 || k.d > 256) return fail(MF_ERR_UNSUPPORTED, "d must be a multiple of 8, at most 256");
   const int64_t e = k.dtype == MF_F32 ? 4 : 2;

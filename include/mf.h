@@ -409,7 +409,7 @@ mf_status mf_cache_stats(mf_block_cache* cache, int64_t* out6);
  * slot, which the slot number no longer tells once an eviction has moved rows.
  *
  * Requirements of all calls: d a multiple of 8, 8..256; K and V 16-byte aligned; page_stride a
- * multiple of 16 bytes; 1 <= nseq <= 4096; 1 <= h_kv <= 64; nseq * max_len below 2^31.
+ * multiple of 16 bytes; 1 <= nseq <= 4096; 1 <= h_kv <= 64; nseq * max_len at most 2^30.
  * ------------------------------------------------------------------------------ */
 typedef struct {
   void* K;                         /* device */
