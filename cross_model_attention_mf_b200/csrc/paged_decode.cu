@@ -673,7 +673,7 @@ __device__ __forceinline__ void add_weights(const DecodeParams& p, int64_t row, 
 template <class Core>
 __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_constant__ DecodeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[WARPS][Core::HT], s_l[WARPS][Core::HT], s_lse2[Core::HT];
+  __shared__ float s_m[WARPS][Core::HT], s_l[WARPS][Core::HT], s_f[WARPS][Core::HT], s_lse2[Core::HT];
   constexpr int RING = Core::STAGES * Core::TILE;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem + warp * RING;
@@ -735,40 +735,52 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
 
     Core::run(p, u, ring, s_m[warp], s_l[warp], warp, lane);
     __syncthreads();
-    // join the warps; a finished unit writes O, a cut one its part
-    const int half = p.d >> 1;
-    for (int i = threadIdx.x; i < u.nh * half; i += NTHR) {
-      const int h = i / half, c = 2 * (i - h * half);
+    // join the warps: their shares first, a head to a thread
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (begins ? 1 : 0);
+    if (threadIdx.x < u.nh) {
+      const int h = threadIdx.x;
       float M = s_m[0][h];
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) M = fmaxf(M, s_m[w][h]);
       const float mu = M == -INFINITY ? 0.0f : M;
-      float L = 0.0f, a = 0.0f, b = 0.0f;
+      float f[WARPS], L = 0.0f;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
-        const float f = ex2(s_m[w][h] - mu);
-        const float* src = reinterpret_cast<const float*>(smem + w * RING) + h * Core::LDB + c;
-        L = fmaf(f, s_l[w][h], L);
-        a = fmaf(f, src[0], a);
-        b = fmaf(f, src[1], b);
+        f[w] = ex2(s_m[w][h] - mu);
+        L = fmaf(f[w], s_l[w][h], L);
       }
+      const float inv = !whole ? 1.0f : L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) s_f[w][h] = f[w] * inv;
       if (whole) {
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        const int64_t at = ((int64_t)u.s * p.h_r + u.h0 + h) * p.d + c;
-        if (p.o_f32) *reinterpret_cast<float2*>(p.O + 4 * at) = make_float2(a * inv, b * inv);
-        else *reinterpret_cast<uint32_t*>(p.O + 2 * at) = pack_bf16(a * inv, b * inv);
-        if (c == 0) {
-          const float v = L == 0.0f ? -INFINITY : mu + log2f(L);
-          const int64_t r = (int64_t)u.s * p.h_r + u.h0 + h;
-          p.lse2[r] = v;
-          if (p.lse) p.lse[r] = v * LN2;
-          s_lse2[h] = v == -INFINITY ? 0.0f : v;
-        }
+        const float v = L == 0.0f ? -INFINITY : mu + log2f(L);
+        const int64_t r = (int64_t)u.s * p.h_r + u.h0 + h;
+        p.lse2[r] = v;
+        if (p.lse) p.lse[r] = v * LN2;
+        s_lse2[h] = v == -INFINITY ? 0.0f : v;
       } else {
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (begins ? 1 : 0);
-        *reinterpret_cast<float2*>(p.part_O + (slot * Core::HT + h) * p.d + c) = make_float2(a, b);
-        if (c == 0) p.part_ml[slot * Core::HT + h] = make_float2(M, L);
+        p.part_ml[slot * Core::HT + h] = make_float2(M, L);
       }
+    }
+    __syncthreads();
+    // a finished unit writes O, a cut one its part
+    const int columns = p.d >> 2;
+    for (int i = threadIdx.x; i < u.nh * columns; i += NTHR) {
+      const int h = i / columns, c = 4 * (i - h * columns);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = s_f[w][h];
+        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * RING) + h * Core::LDB + c);
+        a.x = fmaf(f, v.x, a.x);
+        a.y = fmaf(f, v.y, a.y);
+        a.z = fmaf(f, v.z, a.z);
+        a.w = fmaf(f, v.w, a.w);
+      }
+      const int64_t at = ((int64_t)u.s * p.h_r + u.h0 + h) * p.d + c;
+      if (!whole) *reinterpret_cast<float4*>(p.part_O + (slot * Core::HT + h) * p.d + c) = a;
+      else if (p.o_f32) *reinterpret_cast<float4*>(p.O + 4 * at) = a;
+      else *reinterpret_cast<uint2*>(p.O + 2 * at) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
     }
     __syncthreads();
   }
