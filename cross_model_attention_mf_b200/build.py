@@ -16,7 +16,7 @@ BIND = os.path.join(HERE, "_mf_bind.so")
 BIND_SOURCE = os.path.join(HERE, "csrc", "bind.cpp")
 HEADER = os.path.join(ROOT, "include", "mf.h")
 NVCC_FLAGS = ["-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo",
-              "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
+              "-shared", "--threads", "0", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 
 
 def sources():
