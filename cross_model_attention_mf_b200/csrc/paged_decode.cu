@@ -72,6 +72,8 @@ struct DecodeParams {
   float* part_O;       // [2 grid][HT][d]
   float2* part_ml;     // [2 grid][HT]
   int P, F, groups;    // units of a bundle, bundles of a sequence, groups of CTAs
+  int groups_each;     // groups / F
+  Divider by_P, by_groups;
   int whole;           // every unit is finished by one CTA
   int own_scores;      // and its group has no other unit: the CTA adds up the weights too
 };
@@ -553,7 +555,6 @@ struct CoreF32 {
 };
 
 __device__ __forceinline__ int tiles_of(int len, int tk) { return max(1, (len + tk - 1) / tk); }
-__device__ __forceinline__ int round_up(int n, int to) { return (n + to - 1) / to * to; }
 
 // Tiles before each sequence on the line of one bundle (`pre`, shared memory), and the tiles of a
 // CTA, which are returned.  A sequence of length 0 takes one (empty) tile, so that its outputs
@@ -583,12 +584,12 @@ __device__ inline int64_t scan_tiles(const DecodeParams& p, int tk, int32_t* pre
   int align = 0;
 #pragma unroll
   for (int k = 2; k >= 0; --k)
-    if (s_n[k] <= p.groups / p.F) align = ALIGN << k;
+    if (s_n[k] <= p.groups_each) align = ALIGN << k;
   int base = 0;
   for (int s0 = 0; s0 < kv.nseq; s0 += NTHR) {
     const int s = s0 + threadIdx.x;
     int n = s < kv.nseq ? pre[s] : 0;
-    if (align) n = round_up(n, align);
+    if (align) n = (n + align - 1) & -align;  // a power of two
     int x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -609,7 +610,9 @@ __device__ inline int64_t scan_tiles(const DecodeParams& p, int tk, int32_t* pre
   }
   if (threadIdx.x == 0) pre[kv.nseq] = base;
   __syncthreads();
-  return align ? align : max((int64_t)MIN_TILES, div_floor((int64_t)base * p.F + p.groups - 1, p.groups));
+  if (align) return align;
+  const int64_t up = (int64_t)base * p.F + p.groups - 1;
+  return max((int64_t)MIN_TILES, up >> 31 == 0 ? p.by_groups.of((int)up) : up / p.groups);
 }
 
 // sum of 2^(x - lse2) over the first n of V heads (the others are padding); an empty row, of x = -inf
@@ -682,7 +685,7 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
   await_earlier();
   if (!p.whole || (p.S && !p.own_scores)) allow_later();  // k_decode_join follows
   int64_t x, end;
-  int s = 0;
+  int s = 0, member = 0;
   if (p.whole) {
     // one unit per CTA: nothing to share out
     x = blockIdx.x;
@@ -695,7 +698,9 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
       if (threadIdx.x == 0) *p.per = per;
     }
     const int64_t total = (int64_t)pre[p.kv.nseq] * p.F;
-    x = per * (blockIdx.x / p.P);
+    const int group = p.by_P.of(blockIdx.x);
+    member = blockIdx.x - group * p.P;
+    x = per * group;
     end = min(total, x + per);
     int hi = p.kv.nseq;  // the sequence whose stretch holds x
     while (hi - s > 1) {
@@ -718,8 +723,8 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
     } else {
       const int nt = pre[s + 1] - pre[s];
       const int64_t rel = x - (int64_t)pre[s] * p.F;
-      const int bundle = (int)div_floor(rel, nt);
-      ui = bundle * p.P + (int)(blockIdx.x % p.P);
+      const int bundle = p.F == 1 ? 0 : (int)div_floor(rel, nt);
+      ui = bundle * p.P + member;
       u.t0 = (int)(rel - (int64_t)bundle * nt);
       const int to = (int)min((int64_t)nt, u.t0 + (end - x));
       u.t1 = min(to, tiles_of(u.len, Core::TK));  // past it the stretch is rounded up
@@ -728,7 +733,7 @@ __global__ void __launch_bounds__(NTHR, Core::CTAS) k_decode(const __grid_consta
       x += to - u.t0;
       if (bundle == p.F - 1 && to == nt) ++s;
     }
-    u.hk = ui / p.hb;
+    u.hk = p.hb == 1 ? ui : ui / p.hb;
     const int in_group = (ui - u.hk * p.hb) * Core::HT;
     u.h0 = u.hk * p.G + in_group;
     u.nh = min(Core::HT, p.G - in_group);
@@ -802,7 +807,7 @@ __device__ __forceinline__ Parts unit_parts(const DecodeParams& p, int s, int ui
   if (p.whole) return {0, 1, 1};
   const int before = p.pre[s], nt = p.pre[s + 1] - before;
   const int64_t per = *p.per;
-  const int bundle = ui / p.P;
+  const int bundle = p.by_P.of(ui);
   const int64_t at = (int64_t)before * p.F + (int64_t)bundle * nt;
   const int g0 = (int)div_floor(at, per);
   return {g0 * p.P + (ui - bundle * p.P), p.P, (int)div_floor(at + nt - 1, per) - g0 + 1};
@@ -1005,6 +1010,9 @@ cudaError_t launch_paged_decode(const mf_paged_decode_desc& d, const PagedDecode
     while (p.U % p.P || 20 * (resident / p.P * p.P) < 19 * resident) --p.P;  // 1 leaves none
     p.F = p.U / p.P;
     p.groups = resident / p.P;
+    p.groups_each = p.groups / p.F;
+    p.by_P = Divider(p.P);
+    p.by_groups = Divider(p.groups);
     grid = p.whole ? units : p.groups * p.P;
     const size_t smem = (size_t)WARPS * Core::STAGES * Core::TILE + (p.whole ? 0 : 4 * ((size_t)p.kv.nseq + 1));
     // room for the scan of the largest batch

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "mf_internal.cuh"
@@ -20,6 +21,20 @@ template <auto Kernel> cudaError_t allow_smem(int dev, int bytes) {
   return e;
 }
 
+// n / d by a product, 0 <= n < 2^31: with 2^l >= d and mul = floor(2^(31+l) / d) + 1 the product
+// exceeds n 2^(31+l) / d by at most n 2^l / d, too little to reach the next quotient.
+struct Divider {
+  uint32_t mul;
+  int shift;
+  explicit Divider(int d = 1) {
+    int l = 0;
+    while (((int64_t)1 << l) < d) ++l;
+    shift = 31 + l;
+    mul = (uint32_t)((uint64_t(1) << shift) / (uint64_t)d + 1);
+  }
+  __device__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
+};
+
 struct KvView {
   char* K;
   char* V;
@@ -27,8 +42,8 @@ struct KvView {
   int32_t slot_bytes;  // h_kv * d * element: one slot's rows of every key head
   int32_t row_bytes;   // d * element: one key head's row
   int n_pages, page_size, max_pages, nseq, max_len;
-  uint32_t page_mul;   // n / page_size = n page_mul >> page_shift, 0 <= n < 2^31
-  int page_shift;
+  Divider by_page;     // by page_size
+  int top;             // the longest length: max_len, or the slots of the table
   const int32_t* table;
   const int32_t* lens;
   uint32_t* status;
@@ -44,12 +59,8 @@ inline KvView kv_view(const mf_paged_kv& k, uint32_t* status) {
   v.page_bytes = k.page_stride ? k.page_stride * e : (int64_t)k.page_size * v.slot_bytes;
   v.n_pages = k.n_pages;
   v.page_size = k.page_size;
-  // with 2^l >= page_size and mul = floor(2^(31+l) / page_size) + 1 the product exceeds
-  // n 2^(31+l) / page_size by at most n 2^l / page_size: too little to reach the next quotient
-  int l = 0;
-  while (((int64_t)1 << l) < k.page_size) ++l;
-  v.page_shift = 31 + l;
-  v.page_mul = (uint32_t)((uint64_t(1) << v.page_shift) / (uint64_t)k.page_size + 1);
+  v.by_page = Divider(k.page_size);
+  v.top = (int)std::min<int64_t>(k.max_len, (int64_t)k.max_pages * k.page_size);
   v.max_pages = k.max_pages;
   v.nseq = k.nseq;
   v.max_len = k.max_len;
@@ -63,11 +74,9 @@ inline KvView kv_view(const mf_paged_kv& k, uint32_t* status) {
 // one that is not
 __device__ __forceinline__ int kv_len(const KvView& v, int s, bool report) {
   const int len = v.lens[s];
-  const int64_t room = (int64_t)v.max_pages * v.page_size;
-  const int top = room < v.max_len ? (int)room : v.max_len;
-  if (len >= 0 && len <= top) return len;
+  if ((unsigned)len <= (unsigned)v.top) return len;
   if (report) atomicOr(v.status, ST_INDEX);
-  return len < 0 ? 0 : top;
+  return len < 0 ? 0 : v.top;
 }
 
 // floor of a / b for a >= 0, b > 0 (a 64-bit division takes four times the instructions)
@@ -81,7 +90,7 @@ struct KvPlace {
   int page, row;
 };
 __device__ __forceinline__ KvPlace kv_place(const KvView& v, int slot) {
-  const int page = (int)(((uint64_t)(uint32_t)slot * v.page_mul) >> v.page_shift);
+  const int page = v.by_page.of(slot);
   return {page, slot - page * v.page_size};
 }
 // the page id of sequence s in that place
