@@ -343,9 +343,9 @@ __global__ void __launch_bounds__(NT, 1)
     k_retrieve_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ VMaps tmVs,
                   const __grid_constant__ TcParams p) {
   // Every launch is a programmatic dependent launch.  A later launch of the same call reads
-  // nothing this grid writes, so it may take SMs as soon as this grid's CTAs exit; the call's
-  // first launch waits for the previous kernel on the stream (below, before its first global
-  // access) and only then lets the later launches start.
+  // nothing this grid writes, so it may take SMs as soon as this grid's CTAs exit (and waits for it
+  // at its own end); the call's first launch waits for the previous kernel on the stream (below,
+  // before its first global access) and only then lets the later launches start.
   if (!p.dep_wait) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
@@ -920,6 +920,9 @@ __global__ void __launch_bounds__(NT, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
   }
+  // This launch ends after the one before it, and so after every earlier one of the call: a kernel
+  // that is launched early behind the call waits for its last launch alone.
+  if (!p.dep_wait) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ host side

@@ -408,6 +408,10 @@ mf_status mf_cache_stats(mf_block_cache* cache, int64_t* out6);
  * and int32 pos [nseq][h_kv][stride], stride >= max_len.  pos holds the token position of each
  * slot, which the slot number no longer tells once an eviction has moved rows.
  *
+ * Order: a call starts while the kernel before it in the stream ends and waits for that kernel
+ * before its first access, as mf_map_retrieve does.  A caller's own kernel that was launched as a
+ * programmatic dependent and does not wait for its predecessor needs an ordinary one behind it.
+ *
  * Requirements of all calls: d a multiple of 8, 8..256; K and V 16-byte aligned; page_stride a
  * multiple of 16 bytes; 1 <= nseq <= 4096; 1 <= h_kv <= 64; nseq * max_len at most 2^30.
  * ------------------------------------------------------------------------------ */

@@ -1052,3 +1052,48 @@ def test_captured_calls_after_a_joined_stream():
         for a, b in zip(got, want):
             assert torch.equal(a, b)
     _clean(mf)
+
+
+def test_calls_wait_for_every_layer_of_a_retrieval():
+    """A retrieval of several layers launches them without a wait in between; the append and the
+    eviction right behind it write the first layer's pages, and come after all of it."""
+    mf = _mf()
+    L, B, h_s, h_kv, h_r, d, page, n_layers = 4096, 64, 32, 8, 32, 128, 16, 5
+    values, row_ptr, cols, base = ref.make_bsr((L,), B, h_s, BF, seed=3, share=0.05)
+    bsr = mf.BSR(row_ptr.cuda(), cols.cuda(), values.cuda(), row_ptr[-1:].cuda())
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n_pages = L // page
+    V0 = torch.randn(n_layers, n_pages, page, h_kv, d, generator=g, device="cuda").to(BF)
+    V, K = V0.clone(), torch.zeros_like(V0[0])
+    W = torch.rand(n_layers, h_r, h_s, generator=g, device="cuda") / h_s
+    table = torch.randperm(n_pages, generator=g, device="cuda").to(torch.int32)[None]
+    cu = torch.tensor([0, L], dtype=torch.int32, device="cuda")
+    qb = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv = mf.PagedKV(K, V[0], table, torch.tensor([L], dtype=torch.int32, device="cuda"), L)
+    zeros = torch.zeros(L, h_kv, d, dtype=BF, device="cuda")
+    score = torch.rand(1, h_kv, L, generator=g, device="cuda")
+    pos = torch.arange(L, dtype=torch.int32, device="cuda").expand(1, h_kv, L).contiguous()
+    so, po, lo = torch.empty_like(score), torch.empty_like(pos), torch.empty_like(kv.seq_lens)
+    O = torch.empty(n_layers, L, h_r, d, dtype=BF, device="cuda")
+
+    def retrieve():
+        mf.mf_map_retrieve([bsr], [0] * n_layers, W, V, cu, cu, qb, L, h_r, h_kv, O=O, paged=(table, page),
+                           v_layer_stride=V[0].numel())
+
+    retrieve()
+    torch.cuda.synchronize()
+    want = O.clone()
+    got = []
+    for n in range(12):
+        V.copy_(V0)
+        O.zero_()
+        retrieve()
+        if n % 2:
+            mf.mf_kv_append(kv, zeros, zeros, cu, L)
+        else:
+            mf.mf_kv_evict(kv, score, pos, L // 2, score_out=so, pos_out=po, seq_lens_out=lo)
+        got.append(O.clone())
+    torch.cuda.synchronize()
+    _clean(mf)
+    for n, o in enumerate(got):
+        assert torch.equal(o, want), n
