@@ -925,16 +925,23 @@ __global__ void __launch_bounds__(JOIN_THR, JOIN_CTAS) k_decode_join(const __gri
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
+constexpr int WHOLE_BF16 = 512;  // see whole_keys
+
 // query heads per unit and keys per tile of the kernel that serves a descriptor
 int head_tile(const mf_paged_decode_desc& d) {
-  return d.kv.dtype == MF_BF16 && d.h_r / d.kv.h_kv > 8 ? 16 : 8;
+  if (d.kv.dtype != MF_BF16 || d.h_r / d.kv.h_kv <= 8) return 8;
+  // Groups of more than 8 heads: 16 at a time read the keys once (16 x 8192 tokens, groups of 16:
+  // 92 us, 8 at a time 112).  Few short sequences leave SMs idle, and 8 at a time are done sooner
+  // (32 units of 300 keys 9.1 us, 64 of half the heads 6.6); with weights they would need the join.
+  const bool few = d.kv.max_len <= WHOLE_BF16 && (int64_t)d.kv.nseq * d.kv.h_kv <= 64;
+  return few && !d.score_out ? 8 : 16;
 }
 
 // One CTA per unit, without a second launch, for lengths up to this many keys.  Where units do not
 // fill the GPU, splitting them takes 9 to 10 us at any length: bf16 keys take that long from 512 on
 // (8 tiles a warp), float32 keys from 128 on.  More units than CTAs gain from it a little longer:
 // 512 units of 200 float32 keys 24 us, split 29; of 500 keys 47 and 46.
-int whole_keys(const mf_paged_decode_desc& d, bool fill) { return d.kv.dtype == MF_BF16 ? 512 : fill ? 256 : 128; }
+int whole_keys(const mf_paged_decode_desc& d, bool fill) { return d.kv.dtype == MF_BF16 ? WHOLE_BF16 : fill ? 256 : 128; }
 
 }  // namespace
 
