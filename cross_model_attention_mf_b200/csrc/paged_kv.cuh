@@ -26,7 +26,7 @@ template <auto Kernel> cudaError_t allow_smem(int dev, int bytes) {
 struct Divider {
   uint32_t mul;
   int shift;
-  explicit Divider(int d = 1) {
+  Divider(int d = 1) {
     int l = 0;
     while (((int64_t)1 << l) < d) ++l;
     shift = 31 + l;
