@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
   __shared__ __align__(16) uint32_t s_hist[2][BINS];
   __shared__ __align__(8) uint32_t s_coarse[2][64];
   __shared__ uint32_t s_pick[2][3];           // bin of the smallest kept key, keys to take from it, keys in it
+  __shared__ int s_in[2];                     // the row's length, the tokens seen
   __shared__ uint2 s_cnt[WARPS];              // keys above and at the bar, per warp of the tile
   __shared__ __align__(16) uint32_t s_tot[4]; // of the CTA: above, at the bar; and of those, below the new length
   cg::cluster_group cl = cg::this_cluster();
@@ -180,10 +181,27 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
   const bool first = job == s * p.h_kv && rank == 0 && tid == 0;
   for (int i = tid; i < 2 * BINS / 4; i += THR) reinterpret_cast<uint4*>(s_hist)[i] = make_uint4(0, 0, 0, 0);
   if (tid < 4) s_tot[tid] = 0;
+  if (tid < 6) s_pick[tid / 3][tid % 3] = 0;
   await_earlier();
   allow_later();
-  const int seen = p.n_seen ? p.n_seen[s] : 0;
-  const int len = kv_len(p.kv, s, first);
+  auto sync = [&] {
+    if (SOLO) __syncthreads(); else cl.sync();
+  };
+  int len, seen;
+  if (SOLO) {
+    seen = p.n_seen ? p.n_seen[s] : 0;
+    len = kv_len(p.kv, s, first);
+  } else {
+    // one thread reads the length for the whole cluster: no CTA may leave while others read its
+    // memory, not even if the caller lets the length change meanwhile
+    if (rank == 0 && tid == 0) {
+      s_in[0] = kv_len(p.kv, s, first);
+      s_in[1] = p.n_seen ? p.n_seen[s] : 0;
+    }
+    cl.sync();
+    const int* in0 = cl.map_shared_rank(s_in, 0);
+    len = in0[0], seen = in0[1];
+  }
   // a bound below -2^31 protects every slot, as -2^31 does
   const int recent = (int)max((int64_t)INT32_MIN, (int64_t)(p.n_seen ? seen : len) - p.window);
   const int left = min(len, p.budget);
@@ -205,11 +223,9 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
         if (copy_s) so[j] = sc[j];
         if (copy_p) qo[j] = po[j];
       }
-    return;  // the whole cluster: len is the same for its CTAs
+    if (!SOLO) cl.sync();  // the first CTA's length has been read
+    return;
   }
-  auto sync = [&] {
-    if (SOLO) __syncthreads(); else cl.sync();
-  };
   const bool one = hi - lo <= TILE;
   // Keys of the tile's n slots.  The first pass counts their upper bits, and writes outputs that
   // are not the inputs: slots below the new length as they are (the movers overwrite the holes
@@ -375,7 +391,8 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
     kept_l = __reduce_add_sync(~0u, t.z) + min(need, __reduce_add_sync(~0u, t.w));
   }
   if (!SOLO) cl.barrier_arrive();  // no CTA leaves while another still reads its totals: awaited below
-  if (rank == 0 && tid == 0) p.ws.count[job] = p.budget - (int32_t)kept_l;
+  const int moves = (int)p.ws.moves;
+  if (rank == 0 && tid == 0) p.ws.count[job] = min(max(p.budget - (int32_t)kept_l, 0), moves);
   int32_t* dst = p.ws.dst + (int64_t)job * p.ws.moves;
   int32_t* src = p.ws.src + (int64_t)job * p.ws.moves;
   const uint32_t below = (1u << lane) - 1u;
@@ -408,8 +425,10 @@ __global__ void __launch_bounds__(THR, 1024 / THR) k_evict_select(const __grid_c
       const uint32_t mh = __shfl_sync(~0u, holes, q), mm = __shfl_sync(~0u, movers, q);
       const int ah = __shfl_sync(~0u, at_h, q), am = __shfl_sync(~0u, at_m, q);
       const int j = j0 + 32 * q + lane;
-      if (mh >> lane & 1u) dst[ah + __popc(mh & below)] = j;
-      if (mm >> lane & 1u) src[am + __popc(mm & below)] = j;  // its score and position move with the row
+      // (places within the lists, also if scores change between the passes over a row of several tiles)
+      const int th = ah + __popc(mh & below), tm = am + __popc(mm & below);
+      if ((mh >> lane & 1u) && th >= 0 && th < moves) dst[th] = j;
+      if ((mm >> lane & 1u) && tm < moves) src[tm] = j;  // its score and position move with the row
       if (clear && (__shfl_sync(~0u, gone, q) >> lane & 1u)) {
         so[j] = 0.0f;
         qo[j] = -1;
