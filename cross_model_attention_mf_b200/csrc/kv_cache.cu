@@ -456,15 +456,16 @@ __global__ void __launch_bounds__(MV_THR, 4) k_evict_move(const __grid_constant_
   const int rows = min(MV_ROWS, p.ws.count[job] - m0);
   if (rows <= 0) return;
   const int mine = lane & (MV_ROWS - 1);
-  int slot = 0;
+  int slot = -1;  // of the cache (checked, as the selection's places are)
   int64_t off = -1;
   if (mine < rows) {
     slot = (lane < MV_ROWS ? p.ws.src : p.ws.dst)[(int64_t)job * p.ws.moves + m0 + mine];
-    const int64_t at = kv_slot(p.kv, s, slot);
+    if ((unsigned)slot >= (unsigned)p.kv.top) slot = -1;
+    const int64_t at = slot < 0 ? -1 : kv_slot(p.kv, s, slot);
     if (at >= 0) off = at + (int64_t)g * p.kv.row_bytes;
   }
   const int to_slot = __shfl_down_sync(~0u, slot, MV_ROWS);
-  if (lane < rows) {
+  if (lane < rows && slot >= 0 && to_slot >= 0) {
     const int64_t row = (int64_t)job * p.stride;
     const float sv = p.score_in[row + slot];
     const int pv = p.pos_in[row + slot];
