@@ -20,9 +20,9 @@
 // them in any order.
 //
 // Measured (one B200; copy rate 6469 GB/s): append of 15938 rows of 8 x 128 bf16 for K and V 26.6 us
-// (92%), of 64 rows 3.4 us (launch); one slot out of each of 512 rows of 2049 12.6 us (the selection
-// 11); 16 prompts of 1024 to 8192 tokens cut to 2048 35.7 us (selection 11, moves 22: 117 MB at 82%);
-// 8 rows of 131072 cut to 16384 44.9 us (selection 22 on 64 SMs, moves 21).
+// (92%), of 64 rows 3.5 us (launch); one slot out of each of 512 rows of 2049 12.7 us (the selection
+// 12 of them); 16 prompts of 1024 to 8192 tokens cut to 2048 35.9 us (selection 12, moves 22: 117 MB
+// at 82%); 8 rows of 131072 cut to 16384 46 us (selection 23 on 64 SMs, moves 21).
 #include <cooperative_groups.h>
 #include <stdint.h>
 
