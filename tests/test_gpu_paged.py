@@ -1097,3 +1097,55 @@ def test_calls_wait_for_every_layer_of_a_retrieval():
     _clean(mf)
     for n, o in enumerate(got):
         assert torch.equal(o, want), n
+
+
+def test_two_caches_at_once():
+    """All four calls on two caches, each on a stream of its own with its own workspace, enqueued in
+    turn, from two host threads too: the results are those of one after the other."""
+    import threading
+    mf = _mf()
+    cases = [_order_case(mf) for _ in range(2)]
+    cases[1][0][4].mul_(0.5)  # other queries
+    first = [[t.clone() for t in inputs] for inputs, _, _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+
+    def reset():
+        torch.cuda.synchronize()
+        for (inputs, outs, _), src in zip(cases, first):
+            for t, v in zip(inputs, src):
+                t.copy_(v)
+            for o in outs.values():
+                o.zero_()
+        torch.cuda.synchronize()
+
+    def steps(k, n=3):
+        with torch.cuda.stream(streams[k]):
+            for _ in range(n):
+                cases[k][2]()
+
+    def results():
+        torch.cuda.synchronize()
+        return [[o.clone() for o in outs.values()] + [inputs[0].clone(), inputs[1].clone()] for inputs, outs, _ in cases]
+
+    reset()
+    for k in range(2):
+        steps(k)
+        torch.cuda.synchronize()
+    want = results()
+    assert not torch.equal(want[0][0], want[1][0])
+    for way in ("in turn", "threads"):
+        reset()
+        if way == "in turn":
+            for _ in range(3):
+                for k in range(2):
+                    steps(k, 1)
+        else:
+            threads = [threading.Thread(target=steps, args=(k,)) for k in range(2)]
+            for t in threads:
+                t.start()
+            for t in threads:
+                t.join()
+        for a, b in zip(results(), want):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y), way
+    _clean(mf)
