@@ -91,7 +91,8 @@ mf_dtype dtype_of(const at::Tensor& t) {
 }
 
 // Elements between the rows (dim 0) of one or two tensors, which must agree; their other dims must
-// be dense.  0 for dense rows.
+// be dense.  0 for dense rows, as the C calls take it: rows of an expanded tensor, which are 0 apart,
+// are refused, as all are that begin inside the row before them.
 int64_t row_stride(const at::Tensor& a, const at::Tensor& b, const char* what) {
   if (a.is_contiguous() && b.is_contiguous()) return 0;
   for (const at::Tensor* t : {&a, &b}) {
@@ -100,6 +101,9 @@ int64_t row_stride(const at::Tensor& a, const at::Tensor& b, const char* what) {
       if (t->size(k) != 1 && t->stride(k) != step) refuse(std::string(what) + ": the dims after the first must be dense");
       step *= t->size(k);
     }
+    if (t->size(0) > 1 && t->stride(0) < step)
+      refuse(std::string(what) + " overlap: " + std::to_string(t->stride(0)) + " elements apart, " + std::to_string(step) +
+             " long (an expanded tensor has to be copied first)");
   }
   if (a.size(0) <= 1 || a.numel() == 0) return 0;
   if (a.stride(0) != b.stride(0)) refuse(std::string(what) + " must have the same stride");
@@ -253,7 +257,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     mf_paged_decode_desc d{};
     d.kv = kv.d;
     d.Q = at_address(Q, "Q", kv.dtype, {kv.nseq, h_r, kv.dim}, kv.index, false);
-    d.q_stride = row_stride(Q, Q, "Q");
+    d.q_stride = row_stride(Q, Q, "rows of Q");
     d.h_r = i32(h_r, "h_r");
     d.scale = (float)PyFloat_AsDouble(a[3]);
     if (PyErr_Occurred()) throw Raised{};

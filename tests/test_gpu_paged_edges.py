@@ -1,0 +1,42 @@
+"""The receiver's paged cache at the edges of what its calls allow: rows that overlap, bounds far
+above the lengths, calls of different sizes from several threads, and non-finite keys in sequences
+that are split over the GPU.  Inputs and float64 loops are paged_ref's."""
+import pytest
+import torch
+
+import paged_ref as ref
+from test_gpu_paged import BF, F32, _clean, _kv, _mf
+
+pytestmark = pytest.mark.gpu
+
+
+def test_expanded_rows_are_refused():
+    """Rows of an expanded tensor lie 0 elements apart, which the C calls take for dense rows: a
+    call that went on would read past the one row there is."""
+    mf = _mf()
+    c, _ = ref.make_cache((40, 20, 9), 2, 64, 16, BF, seed=2)
+    kv = _kv(mf, c)
+    cu = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda")
+    q, new = torch.zeros(1, 8, 64, dtype=BF, device="cuda"), torch.zeros(1, 2, 64, dtype=BF, device="cuda")
+    Q, three = q.expand(3, -1, -1), new.expand(3, -1, -1)
+    score, pos = torch.zeros(3, 2, 40, device="cuda"), torch.zeros(3, 2, 40, dtype=torch.int32, device="cuda")
+    page = kv.K[:1].expand(kv.K.shape[0], -1, -1, -1)
+    flat = mf.PagedKV(page, page, kv.block_table, kv.seq_lens, 40)
+    before = kv.K.clone(), kv.V.clone()
+    for call in (lambda: mf.mf_paged_decode(kv, Q),
+                 lambda: mf.mf_paged_decode(kv, q.as_strided((3, 8, 64), (8, 64, 1))),
+                 lambda: mf.mf_kv_append(kv, three, three, cu, 1),
+                 lambda: mf.mf_kv_append(kv, three, three.contiguous(), cu, 1),
+                 lambda: mf.mf_kv_append(kv, three.contiguous(), three, cu, 1),
+                 lambda: mf.mf_paged_decode(flat, Q.contiguous()),
+                 lambda: mf.mf_kv_append(flat, three.contiguous(), three.contiguous(), cu, 1),
+                 lambda: mf.mf_kv_evict(flat, score, pos, 5), flat.desc):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    _clean(mf)
+    assert torch.equal(kv.K, before[0]) and torch.equal(kv.V, before[1])
+    # one row has no neighbour, whatever its stride
+    one = mf.PagedKV(kv.K, kv.V, kv.block_table[:1], kv.seq_lens[:1], 40)
+    got = mf.mf_paged_decode(one, q.as_strided((1, 8, 64), (0, 64, 1)))
+    assert torch.equal(got, mf.mf_paged_decode(one, q))
+    _clean(mf)

@@ -227,3 +227,20 @@ def test_reference_key_scores_match_the_dense_sum():
             dense[:, qb * 32:qb * 32 + 32, int(cols[n]) * 32:int(cols[n]) * 32 + 32] = values[n]
     P = torch.einsum("rs,sij->rij", W.double(), dense)
     assert torch.allclose(out[0], P.sum(1).view(2, 2, 96).sum(1)[:, :70])
+
+
+def test_binding_refuses_overlapping_pages(mf):
+    """Expanded pages lie 0 elements apart, which the C calls would take for dense ones."""
+    from torch._subclasses import FakeTensorMode
+    with FakeTensorMode():
+        t = lambda *shape, dtype=torch.int32: torch.empty(*shape, dtype=dtype, device="cuda")
+        one = t(1, 16, 2, 64, dtype=torch.bfloat16)
+        dense = t(4, 16, 2, 64, dtype=torch.bfloat16)
+        apart = t(4, 2, 16, 2, 64, dtype=torch.bfloat16)[:, 0]
+        desc = lambda K, V: mf.PagedKV(K, V, t(3, 2), t(3), 30).desc()
+        for K, V in ((one.expand(4, -1, -1, -1),) * 2, (dense, one.expand(4, -1, -1, -1)),
+                     (one.expand(4, -1, -1, -1), apart), (dense.as_strided((4, 16, 2, 64), (2040, 128, 64, 1)),) * 2):
+            with pytest.raises(ValueError, match="overlap"):
+                desc(K, V)
+        assert desc(apart, apart).page_stride == 2 * 16 * 2 * 64
+        assert desc(dense, dense).page_stride == 0 and desc(one, one).page_stride == 0
