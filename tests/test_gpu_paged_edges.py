@@ -24,7 +24,7 @@ def test_expanded_rows_are_refused():
     flat = mf.PagedKV(page, page, kv.block_table, kv.seq_lens, 40)
     before = kv.K.clone(), kv.V.clone()
     for call in (lambda: mf.mf_paged_decode(kv, Q),
-                 lambda: mf.mf_paged_decode(kv, q.as_strided((3, 8, 64), (8, 64, 1))),
+                 lambda: mf.mf_paged_decode(kv, torch.cat([q, q]).as_strided((3, 8, 64), (8, 64, 1))),
                  lambda: mf.mf_kv_append(kv, three, three, cu, 1),
                  lambda: mf.mf_kv_append(kv, three, three.contiguous(), cu, 1),
                  lambda: mf.mf_kv_append(kv, three.contiguous(), three, cu, 1),
