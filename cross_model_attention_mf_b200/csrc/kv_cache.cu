@@ -67,9 +67,10 @@ __global__ void __launch_bounds__(AP_THR) k_append(const __grid_constant__ Appen
     return;
   }
   const int t0 = chunk * p.toks, t1 = min(n, t0 + p.toks);
+  if (t0 >= n) return;  // past the sequence's new tokens: max_new may be 2^30, and t1 - t0 far below 0
   const int nv = p.kv.slot_bytes >> 4;
   const int slot0 = len - n;
-  const int work = (t1 - t0) * nv;  // <= 0 past the sequence's new tokens
+  const int work = (t1 - t0) * nv;  // at most toks tokens: AP_VECS vectors, or one token's
   for (int i0 = threadIdx.x; i0 < work; i0 += 4 * AP_THR) {
     uint4 k[4], v[4];
     int64_t to[4];

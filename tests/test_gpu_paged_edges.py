@@ -40,3 +40,26 @@ def test_expanded_rows_are_refused():
     got = mf.mf_paged_decode(one, q.as_strided((1, 8, 64), (0, 64, 1)))
     assert torch.equal(got, mf.mf_paged_decode(one, q))
     _clean(mf)
+
+
+@pytest.mark.parametrize("h_kv,d,dtype,max_new", [(64, 256, F32, 600000), (8, 128, BF, (1 << 24) + 40)])
+def test_append_under_a_bound_far_above_the_new_tokens(h_kv, d, dtype, max_new):
+    """max_new sizes the grid.  A CTA that starts t0 tokens in finds (n - t0) * vectors per token
+    left to copy, which passes -2^31 from t0 = 524290 (64 heads of 256 float32, one token to a CTA)
+    and t0 = 16777224 (8 heads of 128 bf16, 8 tokens) on: it has to stop before that product."""
+    mf = _mf()
+    lens, new = (9, 3, 16), (1, 0, 2)
+    c, _ = ref.make_cache(lens, h_kv, d, 4, dtype, seed=3)
+    kv = _kv(mf, c, max_len=max_new)
+    g = torch.Generator().manual_seed(1)
+    Kn, Vn = (torch.randn(3, h_kv, d, generator=g).to(dtype) for _ in range(2))
+    cu = torch.tensor([0, 1, 1, 3], dtype=torch.int32, device="cuda")
+    mf.mf_kv_append(kv, Kn.cuda(), Vn.cuda(), cu, max_new)
+    _clean(mf)
+    at = 0
+    for s, (n, L) in enumerate(zip(new, lens)):
+        j = torch.arange(L - n, L)
+        idx = (c.table[s].long()[j // 4], j % 4)
+        c.K[idx], c.V[idx] = Kn[at:at + n], Vn[at:at + n]
+        at += n
+    assert torch.equal(kv.K.cpu(), c.K) and torch.equal(kv.V.cpu(), c.V)
