@@ -23,8 +23,9 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
-#include "mf_internal.cuh"
+#include "paged_kv.cuh"
 
 namespace mfi {
 namespace {
@@ -34,6 +35,7 @@ constexpr int CS_THR = 32 * CS_WARPS;
 constexpr int CS_CTAS = 3;     // resident on an SM
 constexpr int CS_GRID = 592;   // most CTAs of k_colsum
 constexpr int CS_HEADS = 32;   // sender heads mixed at a time
+constexpr int MAX_SENDERS = 256, MAX_KEY_HEADS = 64;  // h_s and h_kv, as the entry point checks
 
 struct ColParams {
   const int32_t* row_ptr;
@@ -365,21 +367,23 @@ cudaError_t launch_key_scores(const mf_key_scores_desc& d, const KeyScoresWs& ws
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   p.grid = std::min(CS_GRID, CS_CTAS * sms);
-  const size_t smem = sizeof(float) * ((size_t)d.h_s * d.h_kv + (size_t)d.h_kv * d.B + (size_t)CS_HEADS * d.B);
-  auto launch = [&](auto kern) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return;
-    e = launch_early(kern, p.grid, CS_THR, smem, 1, st, p);
+  auto smem = [&](int h_s, int h_kv) { return sizeof(float) * ((size_t)h_s * h_kv + (size_t)h_kv * d.B + (size_t)CS_HEADS * d.B); };
+  auto launch = [&](auto kernel) {
+    constexpr auto K = decltype(kernel)::value;
+    // the largest call's limit: one of this call's size would fail a larger call of another thread
+    // that has set its own already
+    e = allow_smem<K>(dev, (int)smem(MAX_SENDERS, MAX_KEY_HEADS));
+    if (e == cudaSuccess) e = launch_early(K, p.grid, CS_THR, smem(d.h_s, d.h_kv), 1, st, p);
   };
-  if (d.map_dtype == MF_F32) {
-    if (d.B == 32) launch(k_colsum<float, 32>);
-    else if (d.B == 64) launch(k_colsum<float, 64>);
-    else launch(k_colsum<float, 128>);
-  } else {
-    if (d.B == 32) launch(k_colsum<__nv_bfloat16, 32>);
-    else if (d.B == 64) launch(k_colsum<__nv_bfloat16, 64>);
-    else launch(k_colsum<__nv_bfloat16, 128>);
-  }
+  auto launch_for = [&](auto type) {
+    using T = decltype(type);
+    using std::integral_constant;
+    if (d.B == 32) launch(integral_constant<void (*)(ColParams), &k_colsum<T, 32>>{});
+    else if (d.B == 64) launch(integral_constant<void (*)(ColParams), &k_colsum<T, 64>>{});
+    else launch(integral_constant<void (*)(ColParams), &k_colsum<T, 128>>{});
+  };
+  if (d.map_dtype == MF_F32) launch_for(float{});
+  else launch_for(__nv_bfloat16{});
   if (e != cudaSuccess) return e;
   return launch_early(k_colmerge, (unsigned)((int64_t)p.nseq * p.nqb_max), CM_THR, 4 * (size_t)merge_list(p.nqb_max, p.grid), 1,
                       st, p, d.B);

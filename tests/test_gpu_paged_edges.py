@@ -63,3 +63,45 @@ def test_append_under_a_bound_far_above_the_new_tokens(h_kv, d, dtype, max_new):
         c.K[idx], c.V[idx] = Kn[at:at + n], Vn[at:at + n]
         at += n
     assert torch.equal(kv.K.cpu(), c.K) and torch.equal(kv.V.cpu(), c.V)
+
+
+def test_key_scores_of_two_sizes_from_two_threads():
+    """Calls that share a kernel but not its shared memory, 50 KB apart, enqueued by two host threads:
+    neither may lower the limit that the other one's launch needs."""
+    import threading
+    mf = _mf()
+    B, L = 64, 300
+    cases = []
+    for h_s, h_kv, h_r in ((256, 64, 64), (3, 1, 2)):
+        values, row_ptr, cols, base = ref.make_bsr((L,), B, h_s, BF, seed=h_s)
+        g = torch.Generator().manual_seed(h_s)
+        bsr = mf.BSR(row_ptr.cuda(), cols.cuda(), values.cuda(), row_ptr[-1:].cuda())
+        W = torch.randn(h_r, h_s, generator=g)
+        want, mag = ref.key_scores(values, row_ptr, cols, W, (L,), base, B, h_kv)
+        tol = (B + h_s + h_r // h_kv + 8) * 2.0 ** -23 * mag + 1e-30
+        need = mf.mf_map_key_scores_workspace_size(bsr.capacity, B, h_kv)
+        cases.append((bsr, W.cuda(), h_kv, torch.zeros(1, h_kv, L, device="cuda"), want, tol,
+                      torch.empty(need, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()))
+    cu = torch.tensor([0, L], dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    errors = []
+
+    def calls(case):
+        bsr, W, h_kv, score, _, _, ws, stream = case
+        for _ in range(2000):
+            try:
+                mf.mf_map_key_scores(bsr, W, cu, zero, L, h_kv, score=score, workspace=ws, stream=stream)
+            except mf.MFError as e:
+                errors.append(str(e))
+
+    threads = [threading.Thread(target=calls, args=(c,)) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    _clean(mf)
+    assert not errors, (len(errors), errors[0])
+    for _, _, _, score, want, tol, _, _ in cases:
+        assert ((score.cpu().double() - want).abs() <= tol).all()
