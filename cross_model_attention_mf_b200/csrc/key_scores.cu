@@ -25,7 +25,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "paged_kv.cuh"
+#include "mf_internal.cuh"
 
 namespace mfi {
 namespace {

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 
 #include "mf.h"
@@ -104,6 +105,17 @@ bool launch_calib_gram(const mf_calib_desc& d, void* ws, uint32_t* status, cudaS
                        std::string* err);
 cudaError_t launch_calib_solve(const double* gram, int h_s, int h_r, double ridge, float* W,
                                double* residual, uint32_t* status, cudaStream_t st);
+
+// Raises a kernel's limit of dynamic shared memory to `bytes`, once per device: the most that any
+// call takes, for the limit is the process's, and another thread's call may be about to launch.
+template <auto Kernel> cudaError_t allow_smem(int dev, int bytes) {
+  static std::atomic<uint64_t> done{0};
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Launches of the paged cache's calls overlap with the end of the kernel before them in the stream:
 // every kernel is launched with `launch_early` and waits with `await_earlier`, in every CTA, before

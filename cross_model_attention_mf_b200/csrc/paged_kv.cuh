@@ -5,21 +5,10 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "mf_internal.cuh"
 
 namespace mfi {
-
-// Raises a kernel's limit of dynamic shared memory to `bytes`, once per device.
-template <auto Kernel> cudaError_t allow_smem(int dev, int bytes) {
-  static std::atomic<uint64_t> done{0};
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
-}
 
 // n / d by a product, 0 <= n < 2^31: with 2^l >= d and mul = floor(2^(31+l) / d) + 1 the product
 // exceeds n 2^(31+l) / d by at most n 2^l / d, too little to reach the next quotient.

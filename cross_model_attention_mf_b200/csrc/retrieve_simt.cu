@@ -12,6 +12,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "mf_internal.cuh"
 
 namespace mfi {
@@ -19,6 +21,7 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int MAX_ACC = 64;  // B * d / NT <= 64
+constexpr int MAX_FLOATS = 128 * 128 + NT * MAX_ACC + 256;  // shared memory of the largest B, B * d and h_s
 
 template <typename T> __device__ inline float ld(const T* p);
 template <> __device__ inline float ld<float>(const float* p) { return __ldg(p); }
@@ -164,18 +167,23 @@ cudaError_t launch_retrieve_simt(const mf_retrieve_desc& d, const RetrieveLayer&
   const int64_t grid = (int64_t)d.nseq * p.nqbq * d.h_r;
   if (grid == 0) return cudaSuccess;
   const size_t smem = sizeof(float) * ((size_t)d.B * d.B + (size_t)d.B * d.d + d.h_s);
-  cudaError_t e;
-  auto launch = [&](auto kern) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  auto launch = [&](auto kernel) {
+    constexpr auto K = decltype(kernel)::value;
+    e = allow_smem<K>(dev, (int)sizeof(float) * MAX_FLOATS);
     if (e != cudaSuccess) return;
-    kern<<<(unsigned)grid, NT, smem, st>>>(p);
+    K<<<(unsigned)grid, NT, smem, st>>>(p);
     e = cudaGetLastError();
   };
+  using std::integral_constant;
+  using Kernel = void (*)(SimtParams);
   const bool fa = d.map_dtype == MF_F32, fv = d.v_dtype == MF_F32;
-  if (fa && fv) launch(k_retrieve_simt<float, float>);
-  else if (fa) launch(k_retrieve_simt<float, __nv_bfloat16>);
-  else if (fv) launch(k_retrieve_simt<__nv_bfloat16, float>);
-  else launch(k_retrieve_simt<__nv_bfloat16, __nv_bfloat16>);
+  if (fa && fv) launch(integral_constant<Kernel, &k_retrieve_simt<float, float>>{});
+  else if (fa) launch(integral_constant<Kernel, &k_retrieve_simt<float, __nv_bfloat16>>{});
+  else if (fv) launch(integral_constant<Kernel, &k_retrieve_simt<__nv_bfloat16, float>>{});
+  else launch(integral_constant<Kernel, &k_retrieve_simt<__nv_bfloat16, __nv_bfloat16>>{});
   return e;
 }
 

@@ -105,3 +105,52 @@ def test_key_scores_of_two_sizes_from_two_threads():
     assert not errors, (len(errors), errors[0])
     for _, _, _, score, want, tol, _, _ in cases:
         assert ((score.cpu().double() - want).abs() <= tol).all()
+
+
+def test_float32_retrieval_of_two_sizes_from_two_threads():
+    """mf_map_retrieve's float32 kernel takes B^2 + B d + h_s floats of shared memory: as above."""
+    import ctypes
+    import threading
+    mf = _mf()
+    L = 200
+    cases = []
+    for B, d in ((128, 128), (32, 8)):
+        values, row_ptr, cols, base = ref.make_bsr((L,), B, 3, F32, seed=B)
+        bsr = mf.BSR(row_ptr.cuda(), cols.cuda(), values.cuda(), row_ptr[-1:].cuda())
+        g = torch.Generator().manual_seed(B)
+        W, V = torch.randn(1, 2, 3, generator=g), torch.randn(1, L, 1, d, generator=g)
+        want, mag = torch.zeros(2, 2, L, d, dtype=torch.float64)
+        for qb in range(-(-L // B)):
+            rows = min(B, L - qb * B)
+            for n in range(int(row_ptr[qb]), int(row_ptr[qb + 1])):
+                kb = int(cols[n])
+                A, v = values[n].double()[:, :rows], V[0, kb * B:(kb + 1) * B, 0].double()
+                to = slice(qb * B, qb * B + rows)
+                want[:, to] += torch.einsum("rs,sij,jd->rid", W[0].double(), A[:, :, :len(v)], v)
+                mag[:, to] += torch.einsum("rs,sij,jd->rid", W[0].double().abs(), A[:, :, :len(v)], v.abs())
+        # sums of 3 heads and of L keys, each product and sum rounded once
+        tol = (L + 8) * 2.0 ** -23 * mag + 1e-30
+        cases.append((bsr, W.cuda(), V.cuda(), torch.zeros(1, L, 2, d, device="cuda"), want, tol, torch.cuda.Stream()))
+    cu = torch.tensor([0, L], dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    errors = []
+
+    def calls(case):
+        # through the C call, descriptors at hand: what a call does in Python would keep them apart
+        bsr, W, V, O, _, _, stream = case
+        d, keep = mf._retrieve_desc([bsr], [0], (0, 1), W, V, O, cu, cu, zero, L, 3, bsr.values.shape[2], 2, 1, 0, 0, None, 0)
+        for _ in range(20000):
+            if mf._lib.mf_map_retrieve(ctypes.byref(d), stream.cuda_stream) != mf.MF_OK:
+                errors.append(mf._lib.mf_last_error().decode())
+
+    threads = [threading.Thread(target=calls, args=(c,)) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    _clean(mf)
+    assert not errors, (len(errors), errors[0])
+    for _, _, _, O, want, tol, _ in cases:
+        assert ((O[0].cpu().double().transpose(0, 1) - want).abs() <= tol).all()
