@@ -440,8 +440,8 @@ typedef struct {
  * With score_out, the normalised weights are added up: score_out[s][g][j] = score_in[s][g][j] +
  * sum over the heads r of group g of exp(x_j - lse), j < seq_lens[s]; later slots are left as
  * they were.  score_in may be score_out itself; NULL stands for zeros.
- * Arithmetic: bf16 keys and values run on tensor cores with float32 accumulation, the weights
- * taking part as a bf16 pair (hi + lo, ~16 bits); float32 caches run in float32 throughout.
+ * Arithmetic: bf16 keys and values run on tensor cores with float32 accumulation, each weight
+ * taking part as three bf16 that add up to its 24 bits; float32 caches run in float32 throughout.
  * Softmax statistics are float32.  The keys are split over the GPU by a rule on nseq, h_kv, h_r, d,
  * max_len, the lengths and the number of SMs, and the parts are joined in a fixed order: repeated
  * calls give the same bits.

@@ -154,3 +154,34 @@ def test_float32_retrieval_of_two_sizes_from_two_threads():
     assert not errors, (len(errors), errors[0])
     for _, _, _, O, want, tol, _ in cases:
         assert ((O[0].cpu().double().transpose(0, 1) - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("group", [4, 9])
+def test_weights_enter_the_product_in_float32(group):
+    """O[j] = w_j for values that are unit vectors: the weights as P.V takes them.  Scores are exact
+    (one product of small numbers) and 0, the largest, in every tile of 16 keys, so that nothing is
+    rescaled.  Off are: x in the base-2 domain (its factor and product rounded once each, 2^-23 |x|)
+    and the base-2 exponential (2^-22), in w_j and in the sum of the weights, and one rounding for
+    each of the sums' steps, 2^-24: two tiles of two keys, three exchanges and four warps in l; three
+    terms, the four warps and 1 / l in O, those of the tensor cores taken twice.  A weight of 16 bits
+    would be off by up to 2^-18."""
+    mf = _mf()
+    n, h_kv, d = 128, 4, 128
+    g = torch.Generator().manual_seed(group)
+    K, V = (torch.zeros(1, n, h_kv, d) for _ in range(2))
+    K[0, :, :, 0] = -torch.randint(0, 129, (n, h_kv), generator=g) / 64.0  # x in [-2, 0]
+    K[0, ::16, :, 0] = 0.0
+    V[0] = torch.eye(n)[:, None, :]
+    q = torch.zeros(1, h_kv * group, d)
+    q[..., 0] = 1.0
+    for max_len in (n, 5000):  # one CTA to a unit, and split
+        kv = mf.PagedKV(K.to(BF).cuda(), V.to(BF).cuda(), torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                        torch.tensor([n], dtype=torch.int32, device="cuda"), min(max_len, n))
+        kv.block_table = torch.zeros(1, -(-max_len // n), dtype=torch.int32, device="cuda")
+        kv.max_len = max_len
+        O = mf.mf_paged_decode(kv, q.to(BF).cuda(), scale=1.0, o_f32=True)
+        _clean(mf)
+        want = torch.softmax(K[0, :, :, 0].double(), 0).T.repeat_interleave(group, 0)[None]
+        rel = 2 * (2 * 2.0 ** -23 + 2.0 ** -22) + (2 * 2 + 3 + 4 + 2 * 3 + 4 + 2) * 2.0 ** -24
+        assert rel < 2.0 ** -18
+        assert ((O.double().cpu() - want).abs() <= rel * want).all(), ((O.double().cpu() - want).abs() / want).max()
