@@ -185,3 +185,30 @@ def test_weights_enter_the_product_in_float32(group):
         rel = 2 * (2 * 2.0 ** -23 + 2.0 ** -22) + (2 * 2 + 3 + 4 + 2 * 3 + 4 + 2) * 2.0 ** -24
         assert rel < 2.0 ** -18
         assert ((O.double().cpu() - want).abs() <= rel * want).all(), ((O.double().cpu() - want).abs() / want).max()
+
+
+@pytest.mark.parametrize("group", [4, 9])
+def test_long_sums_are_rounded_to_nearest(group):
+    """Equal weights (Q = 0: scores 0, weights 1, their sum exact) over 8192 positive values of 12
+    powers of two, so that the sums have bits to lose.  With every addition over the tiles rounded
+    to nearest, a result is off by the sum of up to 128 errors, each within 2^-24 of a partial sum
+    and as often up as down: relative to the result their standard deviation is at most
+    2^-24 sqrt(128 / 3) = 6.6 * 2^-24, that of the mean over 1024 columns 2^-24 / 4.8, and six of
+    those are 1.3 * 2^-24.  Only the products of single tiles, cut off once per term at 2^-23 of the
+    tile's sum, go one way, 3 * 2^-23; the joins' few roundings are 2^-23.  Sums over the tiles that
+    are cut off towards zero are off by some 40 * 2^-24 on average."""
+    mf = _mf()
+    n, L, h_kv, d, page = 64, 8192, 8, 128, 16
+    g = torch.Generator().manual_seed(group)
+    V = torch.randn(L // page, page, h_kv, d, generator=g).abs()
+    V = (V * 2.0 ** -torch.randint(0, 12, V.shape, generator=g)).to(BF).cuda()
+    K = torch.randn(L // page, page, h_kv, d, generator=g).to(BF).cuda()
+    # 64 sequences of the same pages: every CTA walks through whole units
+    table = torch.arange(L // page, dtype=torch.int32, device="cuda").expand(n, -1).contiguous()
+    kv = mf.PagedKV(K, V, table, torch.full((n,), L, dtype=torch.int32, device="cuda"), L)
+    O = mf.mf_paged_decode(kv, torch.zeros(n, h_kv * group, d, dtype=BF, device="cuda"), o_f32=True)
+    _clean(mf)
+    want = V.double().flatten(0, 1).mean(0).repeat_interleave(group, 0)[None]
+    off = (O.double() - want) / want
+    assert off.abs().max() <= 128 * 2.0 ** -24
+    assert off.view(n, -1).mean(1).abs().max() <= 1.3 * 2.0 ** -24 + 4 * 2.0 ** -23, off.mean()
