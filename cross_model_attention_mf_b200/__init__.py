@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of the path runs in the CUDA kernels of
 libmf.so.  PyTorch supplies device memory and the current stream.  Importing
-this package fails loudly when libmf.so or _mf_bind.so is missing; there is no fallback.
+this package fails loudly when libmf.so is missing, and so do the paged cache's calls when
+_mf_bind.so is missing or does not fit the installed PyTorch; there is no fallback.
 
 Functions mirror the C entry points:
     mf_compress(...)        -> BSR (row_ptr, col_idx, values, nnz)
@@ -38,11 +39,24 @@ if not os.path.exists(LIB_PATH):
                       "(nvcc, sm_100a); this package has no CPU or library fallback")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+
+class _NoBinding:
+    """Stands in for _mf_bind where it is missing or was built against another PyTorch: the paged
+    cache's calls, which alone need it, raise the reason."""
+
+    def __init__(self, reason):
+        self._reason = reason
+
+    def __getattr__(self, name):
+        raise ImportError("_mf_bind.so is missing or does not fit the installed PyTorch: build it with "
+                          "`python -m cross_model_attention_mf_b200.build`") from self._reason
+
+
 try:
     from . import _mf_bind
 except ImportError as e:
-    raise ImportError("_mf_bind.so is missing or does not fit the installed PyTorch: build it with "
-                      "`python -m cross_model_attention_mf_b200.build`") from e
+    _mf_bind = _NoBinding(e)
 
 MF_OK, MF_ERR_INVALID, MF_ERR_UNSUPPORTED, MF_ERR_CAPACITY, MF_ERR_CUDA, MF_ERR_TIMEOUT, \
     MF_ERR_DEVICE_INDEX = range(7)
@@ -607,9 +621,10 @@ def choose_sender_layer(residuals_per_candidate: Sequence[torch.Tensor]) -> int:
 # ----------------------------------------------------------------------------- paged cache
 
 # the calls below are made by _mf_bind (csrc/bind.cpp), which checks the tensors and fills the descriptors
-_mf_bind.attach({_n: ctypes.cast(getattr(_lib, _n), _P).value for _n in (
-    "mf_paged_decode", "mf_paged_decode_workspace_size", "mf_kv_append", "mf_kv_evict",
-    "mf_kv_evict_workspace_size", "mf_map_key_scores", "mf_map_key_scores_workspace_size")}, _check)
+if not isinstance(_mf_bind, _NoBinding):
+    _mf_bind.attach({_n: ctypes.cast(getattr(_lib, _n), _P).value for _n in (
+        "mf_paged_decode", "mf_paged_decode_workspace_size", "mf_kv_append", "mf_kv_evict",
+        "mf_kv_evict_workspace_size", "mf_map_key_scores", "mf_map_key_scores_workspace_size")}, _check)
 
 
 @dataclass

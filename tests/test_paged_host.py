@@ -244,3 +244,39 @@ def test_binding_refuses_overlapping_pages(mf):
                 desc(K, V)
         assert desc(apart, apart).page_stride == 2 * 16 * 2 * 64
         assert desc(dense, dense).page_stride == 0 and desc(one, one).page_stride == 0
+
+
+@pytest.mark.parametrize("binding", [None, b"not a library"])
+def test_import_without_the_paged_binding(mf, tmp_path, binding):
+    """Only the paged cache's calls need _mf_bind.so, which fits one PyTorch: without it the package
+    imports, the other calls run, and those raise the reason."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    here = os.path.dirname(mf.__file__)
+    to = tmp_path / "cross_model_attention_mf_b200"
+    to.mkdir()
+    for name in ("__init__.py", "libmf.so"):
+        shutil.copy(os.path.join(here, name), to / name)
+    if binding:
+        (to / "_mf_bind.so").write_bytes(binding)
+    code = """
+import torch, cross_model_attention_mf_b200 as mf
+assert mf.mf_version() and mf.mf_map_key_scores_workspace_size(4, 64, 2) > 0
+assert mf.mf_prefix_hashes([1, 2, 3], 2).size == 2
+t = torch.zeros(1)
+kv = mf.PagedKV(t, t, t, t, 1)
+for call in (kv.desc, lambda: mf.mf_paged_decode(kv, t), lambda: mf.mf_kv_append(kv, t, t, t, 1),
+             lambda: mf.mf_kv_evict(kv, t, t, 1), lambda: mf.mf_map_key_scores(None, t, t, t, 1, 1)):
+    try:
+        call()
+    except ImportError as e:
+        assert "_mf_bind.so" in str(e) and isinstance(e.__cause__, ImportError), e
+    else:
+        raise AssertionError("no error")
+print("ok")
+"""
+    run = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True,
+                         env={k: v for k, v in os.environ.items() if k != "MF_LIBRARY"})
+    assert run.returncode == 0 and run.stdout.strip() == "ok", run.stderr
