@@ -35,7 +35,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("MF_LIBRARY") or os.path.join(_HERE, "libmf.so")
 
 if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is missing: build it with `python -m cross_model_attention_mf_b200.build` "
+    # (`python -m` would import this package first)
+    raise ImportError(f"{LIB_PATH} is missing: build it with `python {os.path.join(_HERE, 'build.py')}` "
                       "(nvcc, sm_100a); this package has no CPU or library fallback")
 
 _lib = ctypes.CDLL(LIB_PATH)

@@ -280,3 +280,23 @@ print("ok")
     run = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True,
                          env={k: v for k, v in os.environ.items() if k != "MF_LIBRARY"})
     assert run.returncode == 0 and run.stdout.strip() == "ok", run.stderr
+
+
+def test_import_without_the_library_names_a_way_to_build_it(mf, tmp_path):
+    import os
+    import re
+    import shutil
+    import subprocess
+    import sys
+    to = tmp_path / "cross_model_attention_mf_b200"
+    to.mkdir()
+    for name in ("__init__.py", "build.py"):
+        shutil.copy(os.path.join(os.path.dirname(mf.__file__), name), to / name)
+    run = subprocess.run([sys.executable, "-c", "import cross_model_attention_mf_b200"], cwd=tmp_path,
+                         capture_output=True, text=True, env={k: v for k, v in os.environ.items() if k != "MF_LIBRARY"})
+    script = re.search(r"libmf.so is missing: build it with `python (\S+)`", run.stderr)
+    # the script that it names starts without the package
+    assert run.returncode and script, run.stderr
+    run = subprocess.run([sys.executable, "-c", f"import runpy; print(runpy.run_path({script[1]!r})['LIB'])"],
+                         cwd=tmp_path, capture_output=True, text=True)
+    assert run.stdout.strip() == str(to / "libmf.so"), run.stderr
