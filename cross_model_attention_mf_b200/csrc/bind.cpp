@@ -259,8 +259,10 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.Q = at_address(Q, "Q", kv.dtype, {kv.nseq, h_r, kv.dim}, kv.index, false);
     d.q_stride = row_stride(Q, Q, "rows of Q");
     d.h_r = i32(h_r, "h_r");
-    d.scale = (float)PyFloat_AsDouble(a[3]);
+    const double scale = PyFloat_AsDouble(a[3]);
     if (PyErr_Occurred()) throw Raised{};
+    d.scale = (float)scale;
+    if (scale != 0.0 && d.scale == 0.0f) refuse("scale is too small for a float32 (0 would mean 1 / sqrt(d))");
     const at::Tensor O = a[2] == Py_None ? at::empty({kv.nseq, h_r, kv.dim}, on(kv.index, o_type)) : tensor(a[2], "O");
     d.O = at_address(O, "O", o_type, {kv.nseq, h_r, kv.dim}, kv.index);
     d.lse = at_address<float>(a[4], "lse", at::kFloat, {kv.nseq, h_r}, kv.index);

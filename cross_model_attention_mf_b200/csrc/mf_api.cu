@@ -267,7 +267,8 @@ mf_status check_paged_decode(const mf_paged_decode_desc* d) {
   if (!d->Q || !d->O) return fail(MF_ERR_INVALID, "Q or O is NULL");
   if (d->h_r < 1 || d->h_r % d->kv.h_kv) return fail(MF_ERR_INVALID, "h_r must be a multiple of h_kv");
   if (d->h_r > 256) return fail(MF_ERR_UNSUPPORTED, "h_r must be <= 256");
-  if (!(d->scale >= 0.0f) || std::isinf(d->scale)) return fail(MF_ERR_INVALID, "scale must be finite and >= 0");
+  // (scale log2 e has to be a float32 too)
+  if (!(d->scale >= 0.0f && d->scale <= 0x1p127f)) return fail(MF_ERR_INVALID, "scale must be in [0, 2^127]");
   if (d->flags & ~MF_DECODE_O_F32) return fail(MF_ERR_INVALID, "unknown decode flags");
   if (bad_stride(d->q_stride, (int64_t)d->h_r * d->kv.d, d->kv.dtype == MF_F32 ? 4 : 2))
     return fail(MF_ERR_INVALID, "q_stride must be 0, or cover a row in a multiple of 16 bytes");

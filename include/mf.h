@@ -446,7 +446,7 @@ typedef struct {
  * max_len, the lengths and the number of SMs, and the parts are joined in a fixed order: repeated
  * calls give the same bits.
  * Requirements: h_r a multiple of h_kv, h_r <= 256; Q and O 16-byte aligned, q_stride a multiple
- * of 16 bytes; scale finite and >= 0 (0 means 1 / sqrt(d)). */
+ * of 16 bytes; scale in [0, 2^127] (0 means 1 / sqrt(d)). */
 #define MF_DECODE_O_F32 1            /* flags: O is float32 */
 typedef struct {
   mf_paged_kv kv;

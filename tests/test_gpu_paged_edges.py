@@ -212,3 +212,23 @@ def test_long_sums_are_rounded_to_nearest(group):
     off = (O.double() - want) / want
     assert off.abs().max() <= 128 * 2.0 ** -24
     assert off.view(n, -1).mean(1).abs().max() <= 1.3 * 2.0 ** -24 + 4 * 2.0 ** -23, off.mean()
+
+
+def test_scales_that_are_no_float32_are_refused():
+    """A scale that rounds to 0 as a float32 must not be taken for the default, 1 / sqrt(d)."""
+    mf = _mf()
+    c, _ = ref.make_cache((40, 20), 2, 64, 16, BF, seed=2)
+    kv = _kv(mf, c)
+    Q = torch.randn(2, 8, 64, generator=torch.Generator().manual_seed(1)).to(BF)
+    for scale in (1e-60, -1e-60, 5e-324):
+        with pytest.raises(ValueError, match="too small"):
+            mf.mf_paged_decode(kv, Q.cuda(), scale=scale)
+    for scale in (1e39, 3e38, -1.0, float("nan")):
+        with pytest.raises(mf.MFError, match="scale"):
+            mf.mf_paged_decode(kv, Q.cuda(), scale=scale)
+    # the smallest float32: equal weights
+    O = mf.mf_paged_decode(kv, Q.cuda(), scale=1e-45, o_f32=True)
+    _clean(mf)
+    for s, L in enumerate(c.lens):
+        want = torch.stack([c.rows(c.V, s, g, range(L)).double().mean(0) for g in range(2)])
+        assert ((O[s].cpu().double() - want.repeat_interleave(4, 0)).abs() <= 2.0 ** -20).all()

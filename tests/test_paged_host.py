@@ -300,3 +300,13 @@ def test_import_without_the_library_names_a_way_to_build_it(mf, tmp_path):
     run = subprocess.run([sys.executable, "-c", f"import runpy; print(runpy.run_path({script[1]!r})['LIB'])"],
                          cwd=tmp_path, capture_output=True, text=True)
     assert run.stdout.strip() == str(to / "libmf.so"), run.stderr
+
+
+def test_scales_of_the_base_two_domain_are_bounded(mf):
+    """Scores are multiplied by scale log2 e, a float32: a scale above 2^128 / log2 e would make it
+    infinite, and scores of 0 NaN."""
+    d = decode_desc(mf)
+    n = ctypes.c_size_t(0)
+    for scale, status in ((2.0 ** 127, 0), (1e-45, 0), (0.0, 0), (2.0 ** 127 * 1.0001, 1), (3.4e38, 1)):
+        d.scale = scale
+        assert mf._lib.mf_paged_decode_workspace_size(ctypes.byref(d), ctypes.byref(n)) == status, scale
