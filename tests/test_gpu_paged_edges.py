@@ -1,11 +1,13 @@
 """The receiver's paged cache at the edges of what its calls allow: rows that overlap, bounds far
 above the lengths, calls of different sizes from several threads, and non-finite keys in sequences
 that are split over the GPU.  Inputs and float64 loops are paged_ref's."""
+import math
+
 import pytest
 import torch
 
 import paged_ref as ref
-from test_gpu_paged import BF, F32, _clean, _kv, _mf
+from test_gpu_paged import BF, F32, _clean, _kv, _mf, check_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -232,3 +234,85 @@ def test_scales_that_are_no_float32_are_refused():
     for s, L in enumerate(c.lens):
         want = torch.stack([c.rows(c.V, s, g, range(L)).double().mean(0) for g in range(2)])
         assert ((O[s].cpu().double() - want.repeat_interleave(4, 0)).abs() <= 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("group", [1, 3, 9])
+@pytest.mark.parametrize("max_len", [3000, 6000])
+def test_non_finite_keys_of_split_sequences(dtype, group, max_len):
+    """Sequences long enough to be cut between CTAs, so that empty and NaN parts are joined and the
+    second kernel adds the weights.  Head 0 of sequence 0: every score -inf; of 1: one NaN; of 2:
+    one +inf; of 3: -inf up to slot 2000; of 4: only slot 1700 above -inf; sequence 5 is empty.
+    Every other row, and those of 3 and 4, are those of the keys above -inf alone."""
+    mf = _mf()
+    lens, d, page = (3000, 3000, 3000, 3000, 3000, 0), 64, 16
+    c, _ = ref.make_cache(lens, 2, d, page, F32, seed=group)
+    c.K, c.V = c.K.to(BF).float(), c.V.to(BF).float()  # the same numbers in both types
+    g = torch.Generator().manual_seed(group)
+    h_r = 2 * group
+    Q = (torch.rand(6, h_r, d, generator=g) + 0.5).to(BF).float()  # positive: -inf stays -inf
+
+    def put(s, slots, value):
+        slots = torch.as_tensor(slots)
+        c.K[c.table[s].long()[slots // page], slots % page, 0, 3] = value
+
+    put(0, range(3000), -math.inf)
+    put(1, [2222], math.nan)
+    put(2, [2999], math.inf)
+    put(3, range(2000), -math.inf)
+    put(4, [j for j in range(3000) if j != 1700], -math.inf)
+    kv = mf.PagedKV(c.K.to(dtype).cuda(), c.V.to(dtype).cuda(), c.table.cuda(),
+                    torch.tensor(lens, dtype=torch.int32, device="cuda"), max_len)
+    lse = torch.empty(6, h_r, device="cuda")
+    before = torch.rand(6, 2, max_len, generator=g).cuda()
+    after = torch.full_like(before, 5.0)
+    O = mf.mf_paged_decode(kv, Q.to(dtype).cuda(), lse=lse, score=before, score_out=after, o_f32=True)
+    _clean(mf)
+    O, lse, before, after = (t.cpu().double() for t in (O, lse, before, after))
+    for s, L in enumerate(lens):
+        for h in range(2):
+            heads = slice(h * group, (h + 1) * group)
+            if L == 0 or (s, h) == (0, 0):
+                assert (O[s, heads] == 0).all() and (lse[s, heads] == -math.inf).all()
+                assert torch.equal(after[s, h, :L], before[s, h, :L])
+            elif (s, h) in ((1, 0), (2, 0)):
+                assert O[s, heads].isnan().all() and lse[s, heads].isnan().all() and after[s, h, :L].isnan().all()
+            else:
+                K, V = (c.rows(t, s, h, range(L)).double() for t in (c.K, c.V))
+                some = K[:, 3] > -math.inf
+                K, V, q = K[some], V[some], Q[s, heads].double()
+                x = q @ K.T * d ** -0.5
+                want = torch.logsumexp(x, 1, keepdim=True)
+                w = torch.exp(x - want)
+                # as test_gpu_paged states it
+                dx = (d + 8) * 2.0 ** -23 * d ** -0.5 * (q @ K.abs().T).max()
+                rel = 2 * dx + x.abs().max() * 2.0 ** -22 + 2.0 ** -21 + (L / 16 + 64) * 2.0 ** -24
+                assert ((O[s, heads] - w @ V).abs() <= rel * (w @ V.abs())).all()
+                assert ((lse[s, heads] - want[:, 0]).abs() <= rel + want[:, 0].abs() * 2.0 ** -22).all()
+                gained = torch.zeros(L, dtype=torch.float64)
+                gained[some] = w.sum(0)
+                new = before[s, h, :L] + gained
+                assert ((after[s, h, :L] - new).abs() <= rel * gained + 2.0 ** -23 * new).all()
+                assert torch.equal(after[s, h, :L][~some], before[s, h, :L][~some])
+            assert (after[s, h, L:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens,h_kv,group,d,page", [
+    ((1,), 1, 1, 64, 16), ((0, 1, 15, 16, 17, 33), 2, 4, 128, 16), ((100,), 8, 4, 128, 16),
+    ((300, 0, 1), 8, 3, 128, 64), ((90, 40), 1, 16, 256, 20), ((60, 31), 1, 40, 96, 32),
+])
+def test_short_sequences_under_a_bound_far_above_them(lens, h_kv, group, d, page, dtype):
+    """A captured loop passes its capacity as max_len: short sequences then take the split path."""
+    mf = _mf()
+    c, _ = ref.make_cache(lens, h_kv, d, page, dtype, seed=d, stale=float("nan"))
+    Q = torch.randn(len(lens), h_kv * group, d, generator=torch.Generator().manual_seed(1)).to(dtype)
+    kv = _kv(mf, c, max_len=max(lens) + 4000)
+    kv.block_table = torch.cat([kv.block_table, torch.full((len(lens), 4000 // page + 1), -1, dtype=torch.int32, device="cuda")], 1)
+    lse = torch.empty(len(lens), h_kv * group, device="cuda")
+    before = torch.rand(len(lens), h_kv, kv.max_len, device="cuda")
+    after = before.clone()
+    O = mf.mf_paged_decode(kv, Q.cuda(), lse=lse, score=after)
+    _clean(mf)
+    check_decode(c, Q, O, lse, (before[..., :max(lens) + 1], after[..., :max(lens) + 1]))
+    assert torch.equal(after[..., max(lens):], before[..., max(lens):])
