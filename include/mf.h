@@ -462,8 +462,10 @@ typedef struct {
   int32_t flags;
 } mf_paged_decode_desc;
 
-/* Scratch bytes of mf_paged_decode (depends on nseq, max_len, h_kv, h_r, d and on whether
- * score_out is set; with it, nseq * max_len * h_r * 4 bytes hold the scores x_j). */
+/* Scratch bytes of mf_paged_decode (depends on nseq, max_len, h_kv, h_r, d, the dtype and on
+ * whether score_out is set; with it, nseq * max_len * h_kv * G * 4 bytes hold the scores x_j, G
+ * being h_r / h_kv rounded up to an even number.  It is the bound max_len that counts, not the
+ * lengths: 64 sequences under a bound of 131072 with 32 query heads take 1.1 GB). */
 mf_status mf_paged_decode_workspace_size(const mf_paged_decode_desc* desc, size_t* bytes);
 
 /* Enqueue.  workspace: device, 256-byte aligned, not used by any other call until this one

@@ -310,3 +310,20 @@ def test_scales_of_the_base_two_domain_are_bounded(mf):
     for scale, status in ((2.0 ** 127, 0), (1e-45, 0), (0.0, 0), (2.0 ** 127 * 1.0001, 1), (3.4e38, 1)):
         d.scale = scale
         assert mf._lib.mf_paged_decode_workspace_size(ctypes.byref(d), ctypes.byref(n)) == status, scale
+
+
+@pytest.mark.parametrize("h_r", [2, 4, 6, 8, 18])
+def test_decode_workspace_is_as_documented(mf, h_r):
+    """The scores x_j take nseq * max_len * h_kv * (group rounded up to even) * 4 bytes; groups above
+    8 take more scratch for bf16 (16 heads to a unit) than for float32 (8)."""
+    n, got = ctypes.c_size_t(0), {}
+    for dtype in (0, 1):
+        for scores in (0, A):
+            d = decode_desc(mf)
+            d.kv.dtype, d.kv.max_pages, d.kv.max_len, d.h_r = dtype, 64, 1024, h_r
+            d.score_out, d.score_stride = scores, 1024
+            assert mf._lib.mf_paged_decode_workspace_size(ctypes.byref(d), ctypes.byref(n)) == 0
+            got[dtype, scores] = n.value
+        G = h_r // 2
+        assert got[dtype, A] - got[dtype, 0] == 3 * 1024 * 2 * (G + G % 2) * 4
+    assert (got[1, 0] > got[0, 0]) == (h_r > 16)
