@@ -631,7 +631,7 @@ if not isinstance(_mf_bind, _NoBinding):
 @dataclass
 class PagedKV:
     """Paged key-value cache of one receiver layer (include/mf.h, mf_paged_kv)."""
-    K: torch.Tensor            # [n_pages, page_size, h_kv, d], pages may be strided
+    K: torch.Tensor            # [n_pages, page_size, h_kv, d], pages may be strided, not overlap
     V: torch.Tensor            # as K
     block_table: torch.Tensor  # int32 [nseq, max_pages]
     seq_lens: torch.Tensor     # int32 [nseq]
@@ -669,10 +669,9 @@ def mf_paged_decode(kv: PagedKV, Q: torch.Tensor, O: Optional[torch.Tensor] = No
                     score: Optional[torch.Tensor] = None, score_out: Optional[torch.Tensor] = None,
                     o_f32: bool = False, workspace: Optional[torch.Tensor] = None,
                     stream=None) -> torch.Tensor:
-    """Enqueue attention of one new token per sequence, Q [nseq, h_r, d] (rows may be strided),
-    over the cache; returns O [nseq, h_r, d] (allocated on the call's stream when None; float32
-    with o_f32).  scale 0
-    means 1 / sqrt(d).  lse: float32 [nseq, h_r] out.  score float32 [nseq, h_kv, stride]: the
+    """Enqueue attention of one new token per sequence, Q [nseq, h_r, d] (rows may be strided, but
+    not overlap, as an expanded tensor's do), over the cache; returns O [nseq, h_r, d] (allocated on
+    the call's stream when None; float32 with o_f32).  scale 0 means 1 / sqrt(d).  lse: float32 [nseq, h_r] out.  score float32 [nseq, h_kv, stride]: the
     call's weights are added to it, into score_out when given, else in place; score_out alone
     receives the weights."""
     return _mf_bind.paged_decode(kv, Q, O, scale, lse, score, score_out, o_f32, workspace, stream)
@@ -682,7 +681,7 @@ def mf_kv_append(kv: PagedKV, K_new: torch.Tensor, V_new: torch.Tensor, cu_seqle
                  max_new: int, n_seen: Optional[torch.Tensor] = None,
                  score: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
                  stream=None) -> None:
-    """Enqueue the copy of new tokens' K_new, V_new [T, h_kv, d] (rows may be strided) into the
+    """Enqueue the copy of new tokens' K_new, V_new [T, h_kv, d] (rows as mf_paged_decode's Q) into the
     cache, whose seq_lens already count them; their scores become 0 and their positions
     n_seen - n .. n_seen - 1 where score / pos [nseq, h_kv, stride] are given."""
     _mf_bind.kv_append(kv, K_new, V_new, cu_seqlens_new, max_new, n_seen, score, pos, stream)

@@ -11,11 +11,13 @@
 // next.  The tcgen05 tile (64 rows at least, accumulators in TMEM) would take every score through
 // TMEM and back for a tensor pipe that these loads cannot fill.  float32: FMA.
 //
-// Measured (one B200; copy rate 6469 GB/s): 64 x 8192 tokens, 8 heads of 128, groups of 4, weights
-// carried on: 358 to 370 us, 94 to 91% of that rate; without weights 16 x 8192 tokens 90 us (92%),
-// d = 192 and 256 97%; 131072 tokens with weights 95 us (88%: 87 the main kernel, the rest join and
-// ends that differ by 7 us among CTAs); one sequence of 100 tokens 4.1 us; float32, groups of up to
-// 4, 91%.
+// Measured (one B200; copy rate 6469 GB/s; 8 key heads, bf16, groups of 4 and d = 128 where nothing
+// else is said): 64 x 8192 tokens, weights carried on, 364 to 374 us, 93 to 90% of that rate;
+// 131072 tokens with weights 96 us (88%: 86 the main kernel, the rest join and ends that differ by
+// 7 us among CTAs); 16 x 8192 without weights 87 us (95%), groups of 16 102 (81%), d = 64 55 (75%),
+// 192 130 (96%), 256 176 to 190 (94 to 87%), 256 with groups of 16 294 (56%); 100 tokens 4.0 us,
+// 8.2 under a bound of 8192.  float32, 16 x 4096 tokens: groups of up to 4 91 us (91%), of 8 121 to
+// 125 (67%); d = 64 70 (59%) and 97 (43%): instructions of the exchanges and of shared memory.
 //
 // Split.  A unit is (sequence, key head, block of up to HT query heads of its group).  The units
 // of a sequence go in F bundles of P; the bundles of the batch, cut into tiles of TK keys, lie one
@@ -943,16 +945,20 @@ constexpr int WHOLE_BF16 = 512;  // see whole_keys
 int head_tile(const mf_paged_decode_desc& d) {
   if (d.kv.dtype != MF_BF16 || d.h_r / d.kv.h_kv <= 8) return 8;
   // Groups of more than 8 heads: 16 at a time read the keys once (16 x 8192 tokens, groups of 16:
-  // 92 us, 8 at a time 112).  Few short sequences leave SMs idle, and 8 at a time are done sooner
-  // (32 units of 300 keys 9.1 us, 64 of half the heads 6.6); with weights they would need the join.
+  // 102 us, 8 at a time 118).  Few short sequences leave SMs idle, and 8 at a time are done sooner
+  // (32 key heads of 300 keys 7.0 us, 16 at a time 10.3; 64 of them 7.2 and 10.4; 32 of 512 keys 9.5
+  // and 14.2); with weights they would need the join.
   const bool few = d.kv.max_len <= WHOLE_BF16 && (int64_t)d.kv.nseq * d.kv.h_kv <= 64;
   return few && !d.score_out ? 8 : 16;
 }
 
-// One CTA per unit, without a second launch, for lengths up to this many keys.  Where units do not
-// fill the GPU, splitting them takes 9 to 10 us at any length: bf16 keys take that long from 512 on
-// (8 tiles a warp), float32 keys from 128 on.  More units than CTAs gain from it a little longer:
-// 512 units of 200 float32 keys 24 us, split 29; of 500 keys 47 and 46.
+// One CTA per unit, without a second launch, for bounds max_len up to this many keys: a split call
+// takes 8 us at any length, one CTA's time grows with its keys.  Alone and split, us:
+//   bf16     512 keys: 8 units 8.6 and 8.6, 64 units 9.5 and 11.2, 512 units 25.4 and 29.4;
+//            700 keys: 11.4 and 9.0, 12.4 and 12.9, 32.8 and 36.8;
+//            512 keys with weights: 10.7 and 8.8, 12.9 and 13.3, 32.6 and 35.9;
+//   float32  128 keys: 8 units 6.7 and 8.8, 64 units 7.1 and 9.8; 256 keys: 11.2 and 9.2, 12.0 and 12.1;
+//            512 units, more than CTAs: 256 keys 29.9 and 33.1, 350 keys 38.0 and 41.1.
 int whole_keys(const mf_paged_decode_desc& d, bool fill) { return d.kv.dtype == MF_BF16 ? WHOLE_BF16 : fill ? 256 : 128; }
 
 }  // namespace
