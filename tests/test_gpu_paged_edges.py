@@ -316,3 +316,34 @@ def test_short_sequences_under_a_bound_far_above_them(lens, h_kv, group, d, page
     _clean(mf)
     check_decode(c, Q, O, lse, (before[..., :max(lens) + 1], after[..., :max(lens) + 1]))
     assert torch.equal(after[..., max(lens):], before[..., max(lens):])
+
+
+@pytest.mark.parametrize("own", ["score_out", "pos_out", "seq_lens_out"])
+@pytest.mark.parametrize("lens,budget,h_kv", [((300, 10, 65), 64, 3), ((20000, 16385), 12000, 3), ((140000,), 9000, 1)])
+def test_evict_with_one_output_of_its_own(lens, budget, h_kv, own):
+    """Any of the outputs may be apart from its input while the others are updated in place, and
+    n_seen may be seq_lens itself; rows of one CTA, of a cluster, and of several tiles."""
+    mf = _mf()
+    c, _ = ref.make_cache(lens, h_kv, 64, 16, BF, seed=budget)
+    kv = _kv(mf, c)
+    g = torch.Generator().manual_seed(budget)
+    W = max(lens) + 3
+    score = torch.rand(len(lens), h_kv, W, generator=g)
+    pos = torch.rand(len(lens), h_kv, W, generator=g).argsort(-1).to(torch.int32)
+    sd, pd = score.cuda(), pos.cuda()
+    outs = {"score_out": torch.full_like(sd, 9.0), "pos_out": torch.full_like(pd, 9),
+            "seq_lens_out": torch.full_like(kv.seq_lens, 9)}
+    got = mf.mf_kv_evict(kv, sd, pd, budget, 4, 16, n_seen=kv.seq_lens, **{own: outs[own]})
+    _clean(mf)
+    wscore, wpos, wlens = ref.evict(c, score, pos, list(lens), budget, 4, 16)
+    assert got.tolist() == wlens
+    assert torch.equal(kv.K.cpu(), c.K) and torch.equal(kv.V.cpu(), c.V)
+    so = outs["score_out"] if own == "score_out" else sd
+    po = outs["pos_out"] if own == "pos_out" else pd
+    for s, L in enumerate(lens):
+        assert torch.equal(so[s, :, :L].cpu(), wscore[s, :, :L]) and torch.equal(po[s, :, :L].cpu(), wpos[s, :, :L])
+        assert (so[s, :, L:].cpu() == (9.0 if own == "score_out" else score[s, :, L:])).all()
+        assert (po[s, :, L:].cpu() == (9 if own == "pos_out" else pos[s, :, L:])).all()
+    assert torch.equal(sd.cpu(), score) or own != "score_out"
+    assert torch.equal(pd.cpu(), pos) or own != "pos_out"
+    assert kv.seq_lens.tolist() == list(lens) or own != "seq_lens_out"
